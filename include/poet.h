@@ -398,6 +398,118 @@ poet_status poet_singular_value_entropy(int32_t m, int32_t n, const float* W, in
                                         double* sigma /* [min(m, n)], nullable */, double* entropy /* [1] */,
                                         void* ws, size_t ws_bytes, void* stream);
 
+/* ---- the model's answer: token log-probabilities and distillation ----------------------------------------
+ * What the last linear's output is scored and trained by (the evaluation by perplexity of the Key results; the token
+ * loss whose gradient is the head's dY). Each row of logits z [T x V] (row pitch ld, float32 or bf16) is a distribution
+ *     p = softmax(s z),  s = inv_temp (finite, > 0),
+ * computed in float32 with sums over the row's distance to its maximum m. A row may hold -inf (tokens that cannot
+ * come); a row that holds nothing else has log-probabilities -inf, entropy 0 and gradient 0. A row that holds a NaN or
+ * +inf gives NaN in its float32 results and its gradient. Values are bit-identical from call to call.
+ * The logits and their gradient keep their padding columns [V, ld) untouched. dlogits may be the logits themselves (in
+ * place: same address and pitch); otherwise the two must not overlap (checked: POET_E_ARG). T == 0 does nothing.
+ * V up to POET_MAX_VOCAB (POET_E_UNSUPPORTED above).
+ * ws: at least the matching *_workspace_bytes bytes (0, and ws may be NULL, for most sizes: rows that one workgroup
+ * holds). Calls that share a workspace must be ordered on one stream or by events, as must captured graphs. */
+#define POET_MAX_VOCAB (1 << 24)
+#define POET_MAX_TOP 128 /* largest K: alternatives of a row, entries of a teacher's list */
+typedef struct poet_logits {
+  int32_t T, V;     /* rows (tokens) and vocabulary */
+  int64_t ld;       /* row pitch in elements, >= V */
+  int32_t dtype;    /* POET_F32 or POET_BF16 */
+  float inv_temp;   /* s */
+} poet_logits;
+
+/* Log-probabilities, entropy and best alternatives of each row, and (given their gradients) the logits' gradient:
+ *   ids [T] int32 in, nullable: the token of each row; outside [0, V) (for instance -100): none, log-probability 0.
+ *   logp [T] float32 out, nullable (needs ids): log p[ids].    entropy [T] float32 out, nullable: -sum p log p.
+ *   top_ids, top_logp [T x K] int32 / float32 out (NULL when K == 0; K <= V, K <= POET_MAX_TOP): the K largest logits
+ *     in descending order, equal ones by ascending index (a NaN after everything else), and their log-probabilities.
+ *   stats [T x 4] float32 out: m, log sum exp(s (z - m)), entropy, 0 (kept for the backward; s m + the second is the
+ *     log-partition of the row).
+ *   dlogp, dentropy [T] float32 in, nullable (dlogp needs ids): upstream gradients known before the call. With either
+ *   of them dlogits [T x V] (dtype of the logits, pitch ldd) receives
+ *     dz_j = s ( dlogp (delta_{j, ids} - p_j) - dentropy p_j (log p_j + H) ),
+ *   the same as poet_token_logprobs_bwd writes after the forward, from one reading of the logits where a row fits in a
+ *   workgroup's registers. Without them dlogits must be NULL. The alternatives carry no gradient. */
+size_t poet_token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t dtype, int32_t K);
+poet_status poet_token_logprobs(const poet_logits* L, const void* logits, const int32_t* ids, int32_t K,
+                                const float* dlogp, const float* dentropy, float* logp, float* entropy,
+                                int32_t* top_ids, float* top_logp, float* stats, void* dlogits, int64_t ldd, void* ws,
+                                size_t ws_bytes, void* stream);
+/* The gradient after the forward (for upstream gradients that depend on its results): stats from
+ * poet_token_logprobs on the same logits, ids and inv_temp; dlogp, dentropy nullable, one of them given. */
+poet_status poet_token_logprobs_bwd(const poet_logits* L, const void* logits, const int32_t* ids, const float* stats,
+                                    const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,
+                                    void* stream);
+
+/* Distillation on a teacher's top logits: the Kullback-Leibler divergence of the row's distribution from the
+ * teacher's, which is given by K entries a row (1 <= K <= POET_MAX_TOP), t_ids [T x K] int32 and t_logits [T x K]
+ * float32 (for instance the top_ids and top_logp of poet_token_logprobs on the teacher's logits), with t = t_inv_temp
+ * * t_logits:
+ *   POET_DISTILL_RENORM  q = softmax of t over the row's entries (t_lse must be NULL);
+ *                        loss = sum_k q_k (log q_k - log p_k)
+ *   POET_DISTILL_TAIL    q_k = exp(t_k - t_lse) (t_lse [T] float32, nullable: 0, the entries are log-probabilities);
+ *                        what the list leaves is one more outcome, q_t = max(0, 1 - sum q) against the mass p_t that
+ *                        the student gives to all unlisted tokens:  loss = sum_k q_k (log q_k - log p_k)
+ *                        + q_t (log q_t - log p_t)
+ * An id outside [0, V) is an absent entry; repeated ids add their q; a row without entries has loss 0 and gradient 0.
+ * An entry with q = 0 adds 0; mass on a token that the student cannot give (-inf) makes the loss +inf.
+ *   loss [T] float32 out.   stats [T x 4] float32 out, kept for the backward.
+ *   dloss [T] float32 in, nullable: the rows' upstream gradients; with it dlogits [T x V] (pitch ldd) receives
+ *     dz_j = s dloss (p_j - sum over entries of j of q_k)   listed tokens, and every token of POET_DISTILL_RENORM,
+ *     dz_j = s dloss p_j (1 - q_t / p_t)                    unlisted tokens of POET_DISTILL_TAIL. */
+enum { POET_DISTILL_RENORM = 0, POET_DISTILL_TAIL = 1 };
+typedef struct poet_teacher {
+  int32_t K, mode;
+  float inv_temp; /* finite, > 0 */
+} poet_teacher;
+size_t poet_distill_workspace_bytes(int32_t T, int32_t V, int32_t dtype);
+poet_status poet_distill(const poet_logits* L, const poet_teacher* teacher, const void* logits, const int32_t* t_ids,
+                         const float* t_logits, const float* t_lse, const float* dloss, float* loss, float* stats,
+                         void* dlogits, int64_t ldd, void* ws, size_t ws_bytes, void* stream);
+poet_status poet_distill_bwd(const poet_logits* L, const poet_teacher* teacher, const void* logits,
+                             const int32_t* t_ids, const float* t_logits, const float* t_lse, const float* stats,
+                             const float* dloss, void* dlogits, int64_t ldd, void* stream);
+
+/* ---- the seam between two blocks of linears -----------------------------------------------------------------
+ * The norm after a block, its gate, the scaled residual sum and the norm before the next block in one pass (root mean
+ * square norms, float32 inside), for T tokens of dimension d (1 <= d <= POET_MAX_NORM):
+ *     r_y = (mean(y^2) + eps)^(-1/2),  h_out = round(res_scale h + gate * (r_y y w_post))
+ *     r_h = (mean(h_out^2) + eps)^(-1/2),  x = r_h h_out w_pre
+ * h, h_out [T x ldh] (res_dtype): the residual stream; y [T x ldy] (act_dtype): the block's output; x [T x ldx]
+ * (act_dtype): the next linears' X; w_post, w_pre [d] float32; gate [ceil(T / gate_tokens) x ldg] (act_dtype): one row
+ * for each run of gate_tokens consecutive tokens (1: every token its own; the last run may be short).
+ *   w_post NULL: y is not normalized (r_y = 1, no weight).   gate NULL: 1.
+ *   y NULL (before the first block): h_out, gate and w_post must be NULL too, and x is the norm of h.
+ *   w_pre and x both NULL (after the last block): no second norm.
+ * rstd [T x 2] float32 out: r_y (1 without w_post) and r_h (0 without w_pre), kept for the backward. h_out may be h;
+ * other overlaps of outputs with anything are refused (POET_E_ARG). T == 0 does nothing in the forward. */
+#define POET_MAX_NORM 16384
+typedef struct poet_norm {
+  int32_t T, d;
+  int64_t ldh, ldy, ldg, ldx;      /* row pitches in elements, >= d where their tensor is given */
+  int32_t res_dtype, act_dtype;    /* POET_F32 or POET_BF16 each */
+  int32_t gate_tokens;             /* >= 1 when there is a gate */
+  float res_scale, eps;            /* finite; eps > 0 */
+} poet_norm;
+poet_status poet_block_norm_fwd(const poet_norm* N, const void* h, const void* y, const void* gate, const float* w_post,
+                                const float* w_pre, void* h_out, void* x, float* rstd, void* stream);
+/* The backward, in the forward's terms (h_out: the forward's; h itself when y was NULL). dh_out [T x ldh] res_dtype in,
+ * nullable: the gradient that reaches h_out past this seam; dx [T x ldx] act_dtype in: given exactly when w_pre is (one
+ * of dh_out and dx is required). Out: dh [T x ldh] res_dtype, dy [T x ldy] act_dtype (NULL exactly when the forward had
+ * no y), dgate like gate, dw_post, dw_pre [d] float32 (each given exactly when its input is), all overwritten:
+ *     n = r_h h_out,  u = dx w_pre,  t = dh_out + r_h (u - n mean(u n)),  dh = res_scale t,  dw_pre = sum dx n
+ *     b = r_y y,  v = t gate w_post,  dy = r_y (v - b mean(v b)),  dw_post = sum t gate b,
+ *     dgate = sum over the row's tokens of t w_post b         (without w_post: dy = t gate, dgate = sum t y)
+ * (no y: dh = t). y may be NULL when there is neither gate nor w_post. h_out may be NULL when there is no dx. dh may be
+ * dh_out. Sums over tokens run in a fixed order (bit-identical from call to call). T == 0 zeroes dw_post and dw_pre.
+ * ws: at least poet_block_norm_workspace_bytes(T, d, gate ? gate_tokens : 0) bytes. */
+size_t poet_block_norm_workspace_bytes(int32_t T, int32_t d, int32_t gate_tokens);
+poet_status poet_block_norm_bwd(const poet_norm* N, const void* h_out, const void* y, const void* gate,
+                                const float* w_post, const float* w_pre, const float* rstd, const void* dh_out,
+                                const void* dx, void* dh, void* dy, void* dgate, float* dw_post, float* dw_pre,
+                                void* ws, size_t ws_bytes, void* stream);
+
 /* ---- diagnostics ------------------------------------------------------------------------------------ */
 
 /* One internal GEMM of the library, exposed for kernel-level testing (not part of the layer's hot path):
@@ -445,7 +557,9 @@ enum {
   POET_K_GATHER = 9,     /* FS gathers and scatters of sampled rows / columns (and the sampled-block patch) */
   POET_K_OPTIM = 10,     /* optimizer step on the skew parameters and its moment reset */
   POET_K_DIAG = 11,      /* spectral diagnostics (hyperspherical energy, singular-value entropy) */
-  POET_K_NCLASS = 12
+  POET_K_HEAD = 12,      /* token log-probabilities, distillation and their gradients */
+  POET_K_NORM = 13,      /* block norm seams, forward and backward */
+  POET_K_NCLASS = 14
 };
 /* Start (on != 0: clears previous records) or stop recording a HIP event pair around every kernel launch the
  * library issues, on the launch's own stream. Process-wide; intended for benchmarking, adds one event pair

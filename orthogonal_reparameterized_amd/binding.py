@@ -22,6 +22,8 @@ POET_SIDE_R, POET_SIDE_P = 0, 1
 POET_OP_BUILD, POET_OP_FWD, POET_OP_BWD, POET_OP_MERGE, POET_OP_FWD_ACT, POET_OP_BWD_ACT = range(6)
 POET_MAX_K, POET_MAX_PRIM = 16, 8192
 POET_BUILD_STEP, POET_BUILD_MERGE = 0, 1
+POET_DISTILL_RENORM, POET_DISTILL_TAIL = 0, 1
+POET_MAX_VOCAB, POET_MAX_TOP, POET_MAX_NORM = 1 << 24, 128, 16384
 
 EXPORTS = ("poet_theta_len", "poet_num_prims", "poet_prim_len", "poet_powers_len", "poet_workspace_bytes",
            "poet_sample_workspace_bytes", "poet_build_workspace_bytes", "poet_build_orthogonal",
@@ -36,12 +38,14 @@ EXPORTS = ("poet_theta_len", "poet_num_prims", "poet_prim_len", "poet_powers_len
            "poet_linear_bwd_folded_prims", "poet_fold_group_workspace_bytes", "poet_fold_weights_group",
            "poet_sample_indices_noalloc", "poet_adamw_group", "poet_optimizer_reset_group",
            "poet_spectral_workspace_bytes", "poet_hyperspherical_energy", "poet_singular_value_entropy",
-           "poet_build_orthogonal_exact")
+           "poet_build_orthogonal_exact", "poet_token_logprobs_workspace_bytes", "poet_token_logprobs",
+           "poet_token_logprobs_bwd", "poet_distill_workspace_bytes", "poet_distill", "poet_distill_bwd",
+           "poet_block_norm_fwd", "poet_block_norm_workspace_bytes", "poet_block_norm_bwd")
 POET_NOALLOC_MAX_D = 65536  # largest d poet_sample_indices_noalloc accepts (its device scratch holds d int32 flags)
 POET_K_TOKEN_FWD, POET_K_TOKEN_DX, POET_K_TOKEN_GW, POET_K_CHAIN, POET_K_ADJOINT, POET_K_APPLY, POET_K_CONTRACT, \
-    POET_K_MISC, POET_K_MERGE, POET_K_GATHER, POET_K_OPTIM, POET_K_DIAG = range(12)
+    POET_K_MISC, POET_K_MERGE, POET_K_GATHER, POET_K_OPTIM, POET_K_DIAG, POET_K_HEAD, POET_K_NORM = range(14)
 KCLASS_NAMES = ("token_fwd", "token_dx", "token_gw", "chain", "adjoint", "apply", "contract", "misc", "merge",
-                "gather", "optim", "diag")
+                "gather", "optim", "diag", "head", "norm")
 
 
 class PoetError(RuntimeError):
@@ -69,6 +73,22 @@ class poet_layer(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32), ("T", ctypes.c_int32), ("ldw", ctypes.c_int32),
                 ("ldx", ctypes.c_int32), ("ldy", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
                 ("R", poet_side), ("P", poet_side)]
+
+
+class poet_logits(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("V", ctypes.c_int32), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("inv_temp", ctypes.c_float)]
+
+
+class poet_teacher(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int32), ("mode", ctypes.c_int32), ("inv_temp", ctypes.c_float)]
+
+
+class poet_norm(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("ldh", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("ldg", ctypes.c_int64), ("ldx", ctypes.c_int64), ("res_dtype", ctypes.c_int32),
+                ("act_dtype", ctypes.c_int32), ("gate_tokens", ctypes.c_int32), ("res_scale", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 class poet_gemm_desc(ctypes.Structure):
@@ -168,6 +188,18 @@ def lib() -> ctypes.CDLL:
     L.poet_sample_permutation.restype = ctypes.c_int
     L.poet_gather2d.argtypes = [I32, I32, I32, VP, ctypes.c_int64, I32, I32, VP, VP, VP, ctypes.c_int64, VP]
     L.poet_gather2d.restype = ctypes.c_int
+    I64 = ctypes.c_int64
+    L.poet_token_logprobs_workspace_bytes.argtypes = [I32, I32, I32, I32]
+    L.poet_distill_workspace_bytes.argtypes = [I32, I32, I32]
+    L.poet_block_norm_workspace_bytes.argtypes = [I32, I32, I32]
+    for nm in ("poet_token_logprobs_workspace_bytes", "poet_distill_workspace_bytes", "poet_block_norm_workspace_bytes"):
+        getattr(L, nm).restype = S
+    L.poet_token_logprobs.argtypes = [P(poet_logits), VP, VP, I32, VP, VP, VP, VP, VP, VP, VP, VP, I64, VP, S, VP]
+    L.poet_token_logprobs_bwd.argtypes = [P(poet_logits), VP, VP, VP, VP, VP, VP, I64, VP]
+    L.poet_distill.argtypes = [P(poet_logits), P(poet_teacher), VP, VP, VP, VP, VP, VP, VP, VP, I64, VP, S, VP]
+    L.poet_distill_bwd.argtypes = [P(poet_logits), P(poet_teacher), VP, VP, VP, VP, VP, VP, VP, I64, VP]
+    L.poet_block_norm_fwd.argtypes = [P(poet_norm), VP, VP, VP, VP, VP, VP, VP, VP, VP]
+    L.poet_block_norm_bwd.argtypes = [P(poet_norm), VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, S, VP]
     _lib = L
     return L
 
@@ -721,6 +753,239 @@ def poet_singular_value_entropy(m: int, n: int, W, ldw: int, entropy, sigma=None
                                            _ptr(entropy, "entropy", 8, "float64"), _ptr(ws, "ws", need),
                                            ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "poet_singular_value_entropy")
+
+
+# ---- the model's answer: token log-probabilities and distillation --------------------------------------------
+# Logits and their gradient are 2-D device tensors of float32 or bfloat16 with unit column stride and any row stride;
+# every tensor of a call lives on the current device.
+
+def _on_device(t, name: str, dtype: str):
+    """t is a torch tensor of the given dtype(s) on the current device."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    dt = str(t.dtype)[6:]
+    if dt not in dtype.split("|"):
+        raise TypeError(f"{name} must be {dtype.replace('|', ' or ')}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return dt
+
+
+def _mat(t, name: str, rows: int, cols: int, dtype: str):
+    """(device pointer, row pitch in elements) of a rows x cols tensor with unit column stride; None: (None, 0)."""
+    if t is None:
+        return None, 0
+    _on_device(t, name, dtype)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
+    ld, unit = t.stride()
+    if (cols > 1 and unit != 1) or (rows > 1 and ld < cols):
+        raise ValueError(f"{name} must have unit column stride and a row stride of at least {cols}, got {t.stride()}")
+    return t.data_ptr(), ld if rows > 1 else max(ld, cols)
+
+
+def _vec(t, name: str, shape: tuple, dtype: str, required: bool = False):
+    """Device pointer of a contiguous tensor of exactly this shape (None where it is optional)."""
+    if t is None:
+        if required:
+            raise ValueError(f"{name} is required")
+        return None
+    _on_device(t, name, dtype)
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _scratch(ws, need: int, like, stream):
+    """(pointer, bytes) of the workspace; taken from torch on the current stream when the caller keeps none."""
+    if ws is None:
+        if need == 0:
+            return None, 0, None
+        if stream is not None:
+            raise ValueError(f"a call on a stream of its own needs ws ({need} bytes): memory from torch would be "
+                             "reused by the current stream")
+        ws = _torch().empty(need, dtype=_torch().uint8, device=like.device)
+    else:
+        _on_device(ws, "ws", str(ws.dtype)[6:])
+        if not ws.is_contiguous():
+            raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _logits(logits, inv_temp: float):
+    if logits is None or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D tensor")
+    T, V = logits.shape
+    p, ld = _mat(logits, "logits", T, V, "float32|bfloat16")
+    return p, poet_logits(T, V, ld, POET_F32 if logits.dtype is _torch().float32 else POET_BF16, inv_temp)
+
+
+def _grad(dlogits, logits):
+    return _mat(dlogits, "dlogits", logits.shape[0], logits.shape[1], str(logits.dtype)[6:])
+
+
+def poet_token_logprobs_workspace_bytes(T: int, V: int, dtype: int, K: int) -> int:
+    return int(lib().poet_token_logprobs_workspace_bytes(T, V, dtype, K))
+
+
+def poet_token_logprobs(logits, ids, logp, stats, inv_temp: float = 1.0, entropy=None, top_ids=None, top_logp=None,
+                        dlogp=None, dentropy=None, dlogits=None, ws=None, stream=None):
+    """Per row of logits [T, V] (float32 or bf16): logp [T] = log p[ids] (ids int32; outside [0, V): 0), entropy [T],
+    the K best alternatives top_ids [T, K] int32 / top_logp [T, K], stats [T, 4] for the backward (all float32; None
+    leaves one out, ids and logp together). With dlogp and / or dentropy [T] known beforehand, dlogits [T, V] too."""
+    z, L = _logits(logits, inv_temp)
+    T, V = L.T, L.V
+    K = 0 if top_ids is None else top_ids.shape[-1]
+    need = poet_token_logprobs_workspace_bytes(T, V, L.dtype, K)
+    dz, ldd = _grad(dlogits, logits)
+    wp, wn, ws = _scratch(ws, need, logits, stream)
+    st = lib().poet_token_logprobs(
+        ctypes.byref(L), z, _vec(ids, "ids", (T,), "int32"), K, _vec(dlogp, "dlogp", (T,), "float32"),
+        _vec(dentropy, "dentropy", (T,), "float32"), _vec(logp, "logp", (T,), "float32"),
+        _vec(entropy, "entropy", (T,), "float32"), _vec(top_ids, "top_ids", (T, K), "int32"),
+        _vec(top_logp, "top_logp", (T, K), "float32"), _vec(stats, "stats", (T, 4), "float32", True), dz, ldd, wp, wn,
+        _stream(stream))
+    _check(st, "poet_token_logprobs")
+
+
+def poet_token_logprobs_bwd(logits, ids, stats, dlogp, dlogits, inv_temp: float = 1.0, dentropy=None, stream=None):
+    """The logits' gradient after poet_token_logprobs (its stats; the same logits, ids and inv_temp), for upstream
+    gradients dlogp and / or dentropy [T] that depend on its results. dlogits may be the logits (in place)."""
+    z, L = _logits(logits, inv_temp)
+    T = L.T
+    dz, ldd = _grad(dlogits, logits)
+    st = lib().poet_token_logprobs_bwd(
+        ctypes.byref(L), z, _vec(ids, "ids", (T,), "int32"), _vec(stats, "stats", (T, 4), "float32", True),
+        _vec(dlogp, "dlogp", (T,), "float32"), _vec(dentropy, "dentropy", (T,), "float32"), dz, ldd, _stream(stream))
+    _check(st, "poet_token_logprobs_bwd")
+
+
+def poet_distill_workspace_bytes(T: int, V: int, dtype: int) -> int:
+    return int(lib().poet_distill_workspace_bytes(T, V, dtype))
+
+
+def _teacher(t_ids, t_logits, t_lse, mode, t_inv_temp, T):
+    if t_ids is None or t_ids.dim() != 2:
+        raise ValueError("t_ids must be a 2-D tensor")
+    K = t_ids.shape[1]
+    return poet_teacher(K, mode, t_inv_temp), _vec(t_ids, "t_ids", (T, K), "int32"), \
+        _vec(t_logits, "t_logits", (T, K), "float32", True), _vec(t_lse, "t_lse", (T,), "float32")
+
+
+def poet_distill(logits, t_ids, t_logits, loss, stats, mode: int = 0, inv_temp: float = 1.0, t_inv_temp: float = 1.0,
+                 t_lse=None, dloss=None, dlogits=None, ws=None, stream=None):
+    """loss [T] float32: the divergence of each row of logits [T, V] from a teacher given by its top logits t_ids
+    [T, K] int32, t_logits [T, K] float32 (mode POET_DISTILL_RENORM or POET_DISTILL_TAIL, with t_lse [T]); stats [T, 4]
+    for the backward. With the rows' upstream gradients dloss [T] known beforehand, dlogits [T, V] too."""
+    z, L = _logits(logits, inv_temp)
+    T = L.T
+    teacher, ti, tz, tl = _teacher(t_ids, t_logits, t_lse, mode, t_inv_temp, T)
+    dz, ldd = _grad(dlogits, logits)
+    wp, wn, ws = _scratch(ws, poet_distill_workspace_bytes(T, L.V, L.dtype), logits, stream)
+    st = lib().poet_distill(ctypes.byref(L), ctypes.byref(teacher), z, ti, tz, tl, _vec(dloss, "dloss", (T,), "float32"),
+                            _vec(loss, "loss", (T,), "float32", True), _vec(stats, "stats", (T, 4), "float32", True),
+                            dz, ldd, wp, wn, _stream(stream))
+    _check(st, "poet_distill")
+
+
+def poet_distill_bwd(logits, t_ids, t_logits, stats, dloss, dlogits, mode: int = 0, inv_temp: float = 1.0,
+                     t_inv_temp: float = 1.0, t_lse=None, stream=None):
+    """The logits' gradient after poet_distill (its stats; otherwise the same arguments). dlogits may be the logits."""
+    z, L = _logits(logits, inv_temp)
+    T = L.T
+    teacher, ti, tz, tl = _teacher(t_ids, t_logits, t_lse, mode, t_inv_temp, T)
+    dz, ldd = _grad(dlogits, logits)
+    st = lib().poet_distill_bwd(ctypes.byref(L), ctypes.byref(teacher), z, ti, tz, tl,
+                                _vec(stats, "stats", (T, 4), "float32", True),
+                                _vec(dloss, "dloss", (T,), "float32", True), dz, ldd, _stream(stream))
+    _check(st, "poet_distill_bwd")
+
+
+# ---- the seam between two blocks of linears -------------------------------------------------------------------
+
+def _pitch(kind: str, pairs):
+    """The one row pitch of the given (pointer, pitch) pairs; their tensors must agree in it."""
+    lds = {ld for p, ld in pairs if p is not None}
+    if len(lds) > 1:
+        raise ValueError(f"{kind} must have one row stride, got {sorted(lds)}")
+    return lds.pop() if lds else 0
+
+
+def _norm_desc(T, d, hs, ys, gs, xs, res, act, gate_tokens, res_scale, eps):
+    # T == 1: any pitch describes one row
+    one = (lambda kind, pairs: max([ld for _, ld in pairs])) if T == 1 else _pitch
+    return poet_norm(T, d, one("h, h_out, dh_out and dh", hs), one("y and dy", ys), _pitch("gate and dgate", gs)
+                     if gs[0][0] is None or T > 1 else max(ld for _, ld in gs), one("x or dx", xs), res, act,
+                     gate_tokens, res_scale, eps)
+
+
+def _dt_of(t) -> int:
+    return POET_F32 if t.dtype is _torch().float32 else POET_BF16
+
+
+def poet_block_norm_fwd(h, rstd, y=None, gate=None, w_post=None, w_pre=None, h_out=None, x=None,
+                        res_scale: float = 1.0, eps: float = 1e-6, gate_tokens: int = 1, stream=None):
+    """h_out = res_scale h + gate * norm(y) w_post and x = norm(h_out) w_pre for h [T, d] (float32 or bf16, the
+    residual stream), y [T, d] and x [T, d] (one activation dtype), gate [ceil(T / gate_tokens), d], w_post, w_pre [d]
+    float32; rstd [T, 2] float32 out for the backward. Without y (first seam) x = norm(h) w_pre; without w_post y is
+    added as it is; without w_pre and x (last seam) there is no second norm. h_out may be h."""
+    if h is None or h.dim() != 2:
+        raise ValueError("h must be a 2-D tensor")
+    T, d = h.shape
+    res = str(h.dtype)[6:]
+    a = y if y is not None else x
+    if a is None:
+        raise ValueError("nothing to compute: neither y nor x")
+    act = str(a.dtype)[6:]
+    if gate is not None and gate_tokens < 1:
+        raise ValueError("gate_tokens must be >= 1")
+    hp, op = _mat(h, "h", T, d, "float32|bfloat16"), _mat(h_out, "h_out", T, d, res)
+    yp, xp = _mat(y, "y", T, d, "float32|bfloat16"), _mat(x, "x", T, d, "float32|bfloat16" if y is None else act)
+    gp = _mat(gate, "gate", -(-T // gate_tokens) if gate is not None else 0, d, act)
+    N = _norm_desc(T, d, (hp, op), (yp,), (gp,), (xp,), _dt_of(h), _dt_of(a), gate_tokens, res_scale, eps)
+    st = lib().poet_block_norm_fwd(
+        ctypes.byref(N), hp[0], yp[0], gp[0], _vec(w_post, "w_post", (d,), "float32"),
+        _vec(w_pre, "w_pre", (d,), "float32"), op[0], xp[0], _vec(rstd, "rstd", (T, 2), "float32", True), _stream(stream))
+    _check(st, "poet_block_norm_fwd")
+
+
+def poet_block_norm_workspace_bytes(T: int, d: int, gate_tokens: int = 0) -> int:
+    """gate_tokens: 0 without a gate."""
+    return int(lib().poet_block_norm_workspace_bytes(T, d, gate_tokens))
+
+
+def poet_block_norm_bwd(h_out, rstd, y=None, gate=None, w_post=None, w_pre=None, dh_out=None, dx=None, dh=None,
+                        dy=None, dgate=None, dw_post=None, dw_pre=None, res_scale: float = 1.0, gate_tokens: int = 1,
+                        ws=None, stream=None):
+    """The backward of poet_block_norm_fwd (its h_out and rstd; h itself as h_out when it had no y): from dh_out and
+    dx (one may be missing: no gradient reaches h_out past the seam; no w_pre) to dh [T, d], dy [T, d], dgate like
+    gate, dw_post and dw_pre [d] float32, each given exactly when its input is. dh may be dh_out."""
+    if dh is None or dh.dim() != 2:
+        raise ValueError("dh must be a 2-D tensor")
+    T, d = dh.shape
+    res = str(dh.dtype)[6:]
+    a = next((t for t in (y, dy, dx) if t is not None), None)
+    act = "float32|bfloat16" if a is None else str(a.dtype)[6:]
+    if gate is not None and gate_tokens < 1:
+        raise ValueError("gate_tokens must be >= 1")
+    both = "float32|bfloat16"
+    if a is not None:
+        _on_device(a, "y, dy or dx", both)
+    hp, gh, oh = _mat(h_out, "h_out", T, d, res), _mat(dh_out, "dh_out", T, d, res), _mat(dh, "dh", T, d, both)
+    yp, gy, gx = _mat(y, "y", T, d, act), _mat(dy, "dy", T, d, act), _mat(dx, "dx", T, d, act)
+    rows = -(-T // gate_tokens) if gate is not None else 0
+    gp, gg = _mat(gate, "gate", rows, d, act), _mat(dgate, "dgate", rows, d, act)
+    N = _norm_desc(T, d, (hp, gh, oh), (yp, gy), (gp, gg), (gx,), _dt_of(dh), POET_F32 if a is None else _dt_of(a),
+                   gate_tokens, res_scale, 1.0)
+    wp, wn, ws = _scratch(ws, poet_block_norm_workspace_bytes(T, d, gate_tokens if gate is not None else 0), dh, stream)
+    f32 = lambda t, nm, shape=(d,): _vec(t, nm, shape, "float32")  # noqa: E731
+    st = lib().poet_block_norm_bwd(
+        ctypes.byref(N), hp[0], yp[0], gp[0], f32(w_post, "w_post"), f32(w_pre, "w_pre"), f32(rstd, "rstd", (T, 2)),
+        gh[0], gx[0], oh[0], gy[0], gg[0], f32(dw_post, "dw_post"), f32(dw_pre, "dw_pre"), wp, wn, _stream(stream))
+    _check(st, "poet_block_norm_bwd")
 
 
 def poet_merge(L: poet_layer, W0, W0_shadow, thetaR, thetaP, primR, primP, idxR, idxP, seed: int, linear_id: int,

@@ -301,6 +301,39 @@ hipError_t launch_chain_finalize(const float* theta, int mode, int d, int bp, in
 // blocks with zero columns past bp
 hipError_t launch_delta_bf16(const float* prim, int nprim, int bp, int ldo, __bf16* out, hipStream_t st);
 
+// Rows of logits (token_loss.hip): log-probabilities of given tokens, entropy and best alternatives; distillation on a
+// teacher's list; the gradients. Fields as the arguments of poet_token_logprobs / poet_distill of poet.h (s: inv_temp,
+// ts: the teacher's, ld / ldd: row pitches of z and dz); the launches read and write what is non-null.
+struct TokenArgs {
+  const void* z = nullptr; int64_t ld = 0; int T = 0, V = 0, dt = F32; float s = 1.f;
+  const int32_t* ids = nullptr; const float* dlogp = nullptr; const float* dentropy = nullptr;
+  float* logp = nullptr; float* entropy = nullptr;
+  int K = 0; int32_t* top_ids = nullptr; float* top_logp = nullptr;
+  const int32_t* t_ids = nullptr; const float* t_z = nullptr; const float* t_lse = nullptr; int tail = 0; float ts = 1.f;
+  const float* dloss = nullptr; float* loss = nullptr;
+  float* stats = nullptr;
+  void* dz = nullptr; int64_t ldd = 0;
+};
+hipError_t launch_logprobs(const TokenArgs& a, hipStream_t st);
+hipError_t launch_logprobs_bwd(const TokenArgs& a, hipStream_t st);
+hipError_t launch_distill(const TokenArgs& a, hipStream_t st);
+hipError_t launch_distill_bwd(const TokenArgs& a, hipStream_t st);
+
+// The seam between two blocks of linears (block_norm.hip), fields as the arguments of poet_block_norm_fwd / _bwd (h in
+// the backward: the forward's h_out).
+struct NormArgs {
+  int T = 0, d = 0; int64_t ldh = 0, ldy = 0, ldg = 0, ldx = 0;
+  int res_dt = F32, act_dt = F32, gate_tokens = 1; float res_scale = 1.f, eps = 0.f;
+  const void* h = nullptr; const void* y = nullptr; const void* gate = nullptr;
+  const float* w_post = nullptr; const float* w_pre = nullptr;
+  void* h_out = nullptr; void* x = nullptr; float* rstd = nullptr;
+  const void* dh_out = nullptr; const void* dx = nullptr;
+  void* dh = nullptr; void* dy = nullptr; void* dgate = nullptr; float* dw_post = nullptr; float* dw_pre = nullptr;
+};
+size_t block_norm_bytes(int T, int d, int gate_tokens);  // scratch of launch_norm_bwd (gate_tokens 0: no gate)
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st);
+hipError_t launch_norm_bwd(const NormArgs& a, void* ws, hipStream_t st);
+
 // Matrix-core rate probe (mfma_probe.hip): workgroups x 8 waves, each issuing 4 x iters bf16 MFMAs of 32 x 32 x 16 on
 // registers; out receives one float per wave (workgroups x 8).
 hipError_t launch_mfma_probe(int64_t iters, int workgroups, float* out, hipStream_t st);

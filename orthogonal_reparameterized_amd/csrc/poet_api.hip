@@ -2211,6 +2211,259 @@ poet_status poet_merge_group(int32_t count, const poet_layer* layers, float* con
   return POET_OK;
 }
 
+// ---- the model's answer: rows of logits ------------------------------------------------------------------------
+
+static bool finite_pos(float x) { return x > 0.f && x - x == 0.f; }
+
+// Whether two row-strided regions (rows of w bytes at pitch p from base) share a byte. Regions of one pitch may be
+// interleaved columns of one buffer; any other crossing of address ranges counts as an overlap.
+static bool regions_meet(const void* a, int64_t ra, int64_t pa, int64_t wa, const void* b, int64_t rb, int64_t pb, int64_t wb) {
+  if (!a || !b || ra < 1 || rb < 1 || wa < 1 || wb < 1) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t a1 = a0 + (ra - 1) * pa + wa, b1 = b0 + (rb - 1) * pb + wb;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (pa != pb) return true;
+  const int64_t off = (int64_t)((b0 >= a0 ? b0 - a0 : a0 - b0) % (uintptr_t)pa);
+  return b0 >= a0 ? off < wa || off + wb > pa : off < wb || off + wa > pa;
+}
+
+// rows * ld elements, and their bytes, are far from overflowing 64 bits
+static bool rows_fit(int64_t rows, int64_t ld) { return rows < 1 || ld <= ((int64_t)1 << 48) / rows; }
+
+static bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+static bool logits_info(const poet_logits* L) {
+  if (!L) return fail(POET_E_ARG, "null logits description"), false;
+  if (L->dtype != POET_F32 && L->dtype != POET_BF16) return fail(POET_E_DTYPE, "bad dtype %d", L->dtype), false;
+  if (L->T < 0 || L->V < 1) return fail(POET_E_SHAPE, "T = %d must be >= 0 and V = %d >= 1", L->T, L->V), false;
+  if (L->V > POET_MAX_VOCAB) return fail(POET_E_UNSUPPORTED, "V = %d > %d", L->V, POET_MAX_VOCAB), false;
+  if (L->ld < L->V) return fail(POET_E_SHAPE, "ld = %lld too small for V = %d", (long long)L->ld, L->V), false;
+  if (!rows_fit(L->T, L->ld)) return fail(POET_E_UNSUPPORTED, "ld = %lld too large", (long long)L->ld), false;
+  if (!finite_pos(L->inv_temp)) return fail(POET_E_ARG, "inv_temp = %g must be finite and > 0", L->inv_temp), false;
+  return true;
+}
+
+// the logits and their gradient: pitches, alignment to an element, in place or apart
+static bool grad_info(const poet_logits* L, const void* z, const void* dz, int64_t ldd) {
+  const size_t e = dtype_size(L->dtype);
+  if (!z || !aligned(z, e)) return fail(POET_E_ARG, "logits null or not aligned to an element"), false;
+  if (!dz) return true;
+  if (!aligned(dz, e)) return fail(POET_E_ARG, "dlogits not aligned to an element"), false;
+  if (ldd < L->V || !rows_fit(L->T, ldd)) return fail(POET_E_SHAPE, "ldd = %lld for V = %d", (long long)ldd, L->V), false;
+  if (dz == z && ldd == L->ld) return true;
+  const int64_t w = (int64_t)L->V * e;
+  if (regions_meet(z, L->T, L->ld * e, w, dz, L->T, ldd * e, w))
+    return fail(POET_E_ARG, "dlogits overlaps the logits and is not in place"), false;
+  return true;
+}
+
+static TokenArgs token_args(const poet_logits* L, const void* z) {
+  TokenArgs a;
+  a.z = z; a.ld = L->ld; a.T = L->T; a.V = L->V; a.dt = L->dtype; a.s = L->inv_temp;
+  return a;
+}
+
+size_t poet_token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t dtype, int32_t K) {
+  const poet_logits L{T, V, V, dtype, 1.f};
+  if (!logits_info(&L)) return 0;
+  if (K < 0 || K > V || K > POET_MAX_TOP) return fail(POET_E_SHAPE, "K = %d for V = %d (at most %d)", K, V, POET_MAX_TOP), 0;
+  return 0;
+}
+
+poet_status poet_token_logprobs(const poet_logits* L, const void* logits, const int32_t* ids, int32_t K,
+                                const float* dlogp, const float* dentropy, float* logp, float* entropy,
+                                int32_t* top_ids, float* top_logp, float* stats, void* dlogits, int64_t ldd, void* ws,
+                                size_t ws_bytes, void* stream) {
+  if (!logits_info(L)) return g_last;
+  if (K < 0 || K > L->V || K > POET_MAX_TOP)
+    return fail(POET_E_SHAPE, "K = %d for V = %d (at most %d)", K, L->V, POET_MAX_TOP);
+  if ((dlogits != nullptr) != (dlogp || dentropy))
+    return fail(POET_E_ARG, "dlogits goes with dlogp or dentropy, and with them only");
+  if (L->T == 0) return POET_OK;
+  if ((logp || dlogp) && !ids) return fail(POET_E_ARG, "logp and dlogp need ids");
+  if (!grad_info(L, logits, dlogits, ldd)) return g_last;
+  if (!stats) return fail(POET_E_ARG, "null stats");
+  if (K > 0 ? !top_ids || !top_logp : top_ids || top_logp)
+    return fail(POET_E_ARG, "top_ids and top_logp go with K > 0");
+  if (!check_ws(ws, ws_bytes, poet_token_logprobs_workspace_bytes(L->T, L->V, L->dtype, K))) return g_last;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  TokenArgs a = token_args(L, logits);
+  a.ids = ids; a.K = K; a.dlogp = dlogp; a.dentropy = dentropy; a.logp = logp; a.entropy = entropy;
+  a.top_ids = top_ids; a.top_logp = top_logp; a.stats = stats; a.dz = dlogits; a.ldd = ldd;
+  HIP_TRY(launch_logprobs(a, st));
+  if (dlogits) HIP_TRY(launch_logprobs_bwd(a, st));
+  return POET_OK;
+}
+
+poet_status poet_token_logprobs_bwd(const poet_logits* L, const void* logits, const int32_t* ids, const float* stats,
+                                    const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,
+                                    void* stream) {
+  if (!logits_info(L)) return g_last;
+  if (L->T == 0) return POET_OK;
+  if (!dlogp && !dentropy) return fail(POET_E_ARG, "one of dlogp and dentropy is required");
+  if (dlogp && !ids) return fail(POET_E_ARG, "dlogp needs ids");
+  if (!stats || !dlogits) return fail(POET_E_ARG, "null stats or dlogits");
+  if (!grad_info(L, logits, dlogits, ldd)) return g_last;
+  TokenArgs a = token_args(L, logits);
+  a.ids = ids; a.dlogp = dlogp; a.dentropy = dentropy; a.stats = const_cast<float*>(stats); a.dz = dlogits; a.ldd = ldd;
+  HIP_TRY(launch_logprobs_bwd(a, reinterpret_cast<hipStream_t>(stream)));
+  return POET_OK;
+}
+
+static bool teacher_info(const poet_teacher* t, const float* t_lse) {
+  if (!t) return fail(POET_E_ARG, "null teacher"), false;
+  if (t->K < 1 || t->K > POET_MAX_TOP) return fail(POET_E_SHAPE, "K = %d must be in [1, %d]", t->K, POET_MAX_TOP), false;
+  if (t->mode != POET_DISTILL_RENORM && t->mode != POET_DISTILL_TAIL) return fail(POET_E_ARG, "bad mode %d", t->mode), false;
+  if (!finite_pos(t->inv_temp)) return fail(POET_E_ARG, "teacher inv_temp = %g must be finite and > 0", t->inv_temp), false;
+  if (t->mode == POET_DISTILL_RENORM && t_lse) return fail(POET_E_ARG, "t_lse goes with POET_DISTILL_TAIL"), false;
+  return true;
+}
+
+size_t poet_distill_workspace_bytes(int32_t T, int32_t V, int32_t dtype) {
+  const poet_logits L{T, V, V, dtype, 1.f};
+  if (!logits_info(&L)) return 0;
+  return 0;
+}
+
+poet_status poet_distill(const poet_logits* L, const poet_teacher* teacher, const void* logits, const int32_t* t_ids,
+                         const float* t_logits, const float* t_lse, const float* dloss, float* loss, float* stats,
+                         void* dlogits, int64_t ldd, void* ws, size_t ws_bytes, void* stream) {
+  if (!logits_info(L) || !teacher_info(teacher, t_lse)) return g_last;
+  if ((dlogits != nullptr) != (dloss != nullptr)) return fail(POET_E_ARG, "dlogits goes with dloss");
+  if (L->T == 0) return POET_OK;
+  if (!t_ids || !t_logits || !loss || !stats) return fail(POET_E_ARG, "null t_ids, t_logits, loss or stats");
+  if (!grad_info(L, logits, dlogits, ldd)) return g_last;
+  if (!check_ws(ws, ws_bytes, poet_distill_workspace_bytes(L->T, L->V, L->dtype))) return g_last;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  TokenArgs a = token_args(L, logits);
+  a.K = teacher->K; a.t_ids = t_ids; a.t_z = t_logits; a.t_lse = t_lse; a.tail = teacher->mode == POET_DISTILL_TAIL;
+  a.ts = teacher->inv_temp; a.dloss = dloss; a.loss = loss; a.stats = stats; a.dz = dlogits; a.ldd = ldd;
+  HIP_TRY(launch_distill(a, st));
+  if (dlogits) HIP_TRY(launch_distill_bwd(a, st));
+  return POET_OK;
+}
+
+poet_status poet_distill_bwd(const poet_logits* L, const poet_teacher* teacher, const void* logits,
+                             const int32_t* t_ids, const float* t_logits, const float* t_lse, const float* stats,
+                             const float* dloss, void* dlogits, int64_t ldd, void* stream) {
+  if (!logits_info(L) || !teacher_info(teacher, t_lse)) return g_last;
+  if (L->T == 0) return POET_OK;
+  if (!t_ids || !t_logits || !stats || !dloss || !dlogits)
+    return fail(POET_E_ARG, "null t_ids, t_logits, stats, dloss or dlogits");
+  if (!grad_info(L, logits, dlogits, ldd)) return g_last;
+  TokenArgs a = token_args(L, logits);
+  a.K = teacher->K; a.t_ids = t_ids; a.t_z = t_logits; a.t_lse = t_lse; a.tail = teacher->mode == POET_DISTILL_TAIL;
+  a.ts = teacher->inv_temp; a.dloss = dloss; a.stats = const_cast<float*>(stats); a.dz = dlogits; a.ldd = ldd;
+  HIP_TRY(launch_distill_bwd(a, reinterpret_cast<hipStream_t>(stream)));
+  return POET_OK;
+}
+
+// ---- the seam between two blocks of linears ----------------------------------------------------------------------
+
+static bool norm_info(const poet_norm* N, bool gate) {
+  if (!N) return fail(POET_E_ARG, "null norm description"), false;
+  if ((N->res_dtype != POET_F32 && N->res_dtype != POET_BF16) || (N->act_dtype != POET_F32 && N->act_dtype != POET_BF16))
+    return fail(POET_E_DTYPE, "bad res_dtype %d or act_dtype %d", N->res_dtype, N->act_dtype), false;
+  if (N->T < 0 || N->d < 1) return fail(POET_E_SHAPE, "T = %d must be >= 0 and d = %d >= 1", N->T, N->d), false;
+  if (N->d > POET_MAX_NORM) return fail(POET_E_UNSUPPORTED, "d = %d > %d", N->d, POET_MAX_NORM), false;
+  if (gate && N->gate_tokens < 1) return fail(POET_E_SHAPE, "gate_tokens = %d must be >= 1", N->gate_tokens), false;
+  if (!finite_pos(N->eps)) return fail(POET_E_ARG, "eps = %g must be finite and > 0", N->eps), false;
+  if (N->res_scale - N->res_scale != 0.f) return fail(POET_E_ARG, "res_scale = %g must be finite", N->res_scale), false;
+  return true;
+}
+
+struct NormTensor { const char* name; const void* p; int64_t rows, ld; size_t e; };
+
+static bool norm_tensor(const NormTensor& t, int d) {
+  if (!t.p) return true;
+  if (t.ld < d || !rows_fit(t.rows, t.ld)) return fail(POET_E_SHAPE, "%s: pitch %lld for d = %d", t.name, (long long)t.ld, d), false;
+  if (!aligned(t.p, t.e)) return fail(POET_E_ARG, "%s is not aligned to an element", t.name), false;
+  return true;
+}
+
+static bool norm_apart(const NormTensor& a, const NormTensor& b, int d) {
+  if (!regions_meet(a.p, a.rows, a.ld * a.e, (int64_t)d * a.e, b.p, b.rows, b.ld * b.e, (int64_t)d * b.e)) return true;
+  return fail(POET_E_ARG, "%s overlaps %s", a.name, b.name), false;
+}
+
+static NormArgs norm_args(const poet_norm* N) {
+  NormArgs a;
+  a.T = N->T; a.d = N->d; a.ldh = N->ldh; a.ldy = N->ldy; a.ldg = N->ldg; a.ldx = N->ldx;
+  a.res_dt = N->res_dtype; a.act_dt = N->act_dtype; a.gate_tokens = N->gate_tokens; a.res_scale = N->res_scale;
+  a.eps = N->eps;
+  return a;
+}
+
+poet_status poet_block_norm_fwd(const poet_norm* N, const void* h, const void* y, const void* gate, const float* w_post,
+                                const float* w_pre, void* h_out, void* x, float* rstd, void* stream) {
+  if (!norm_info(N, gate != nullptr)) return g_last;
+  if (N->T == 0) return POET_OK;
+  if (y ? !h_out : gate || w_post || h_out)
+    return fail(POET_E_ARG, y ? "y needs h_out" : "gate, w_post and h_out need y");
+  if ((w_pre != nullptr) != (x != nullptr)) return fail(POET_E_ARG, "w_pre and x go together");
+  if (!y && !x) return fail(POET_E_ARG, "nothing to compute: neither y nor x");
+  if (!h || !rstd) return fail(POET_E_ARG, "null h or rstd");
+  const size_t er = dtype_size(N->res_dtype), ea = dtype_size(N->act_dtype);
+  const int64_t grows = gate ? ((int64_t)N->T + N->gate_tokens - 1) / N->gate_tokens : 0;
+  const NormTensor in[] = {{"h", h, N->T, N->ldh, er}, {"y", y, N->T, N->ldy, ea}, {"gate", gate, grows, N->ldg, ea}};
+  const NormTensor out[] = {{"h_out", h_out, N->T, N->ldh, er}, {"x", x, N->T, N->ldx, ea}};
+  for (const auto& t : in) if (!norm_tensor(t, N->d)) return g_last;
+  for (const auto& t : out) if (!norm_tensor(t, N->d)) return g_last;
+  for (const auto& o : out)
+    for (const auto& i : in)
+      if (!(o.p == h_out && i.p == h && h == h_out) && !norm_apart(o, i, N->d)) return g_last;
+  if (!norm_apart(out[0], out[1], N->d)) return g_last;
+  NormArgs a = norm_args(N);
+  a.h = h; a.y = y; a.gate = gate; a.w_post = w_post; a.w_pre = w_pre; a.h_out = h_out; a.x = x; a.rstd = rstd;
+  HIP_TRY(launch_norm_fwd(a, reinterpret_cast<hipStream_t>(stream)));
+  return POET_OK;
+}
+
+size_t poet_block_norm_workspace_bytes(int32_t T, int32_t d, int32_t gate_tokens) {
+  if (T < 0 || d < 1 || d > POET_MAX_NORM || gate_tokens < 0)
+    return fail(POET_E_SHAPE, "T = %d, d = %d (at most %d), gate_tokens = %d", T, d, POET_MAX_NORM, gate_tokens), 0;
+  return T == 0 ? 0 : block_norm_bytes(T, d, gate_tokens) + 256;
+}
+
+poet_status poet_block_norm_bwd(const poet_norm* N, const void* h_out, const void* y, const void* gate,
+                                const float* w_post, const float* w_pre, const float* rstd, const void* dh_out,
+                                const void* dx, void* dh, void* dy, void* dgate, float* dw_post, float* dw_pre,
+                                void* ws, size_t ws_bytes, void* stream) {
+  if (!norm_info(N, gate != nullptr)) return g_last;
+  if ((w_post != nullptr) != (dw_post != nullptr) || (w_pre != nullptr) != (dw_pre != nullptr))
+    return fail(POET_E_ARG, "each weight goes with its gradient");
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (N->T == 0) {
+    if (dw_post) HIP_TRY(launch_fill(dw_post, N->d, 0.f, st));
+    if (dw_pre) HIP_TRY(launch_fill(dw_pre, N->d, 0.f, st));
+    return POET_OK;
+  }
+  if ((w_pre != nullptr) != (dx != nullptr)) return fail(POET_E_ARG, "dx goes with w_pre");
+  if ((gate != nullptr) != (dgate != nullptr)) return fail(POET_E_ARG, "dgate goes with gate");
+  if ((gate || w_post) && (!y || !dy)) return fail(POET_E_ARG, "gate and w_post need y and dy");
+  if (!dh_out && !dx) return fail(POET_E_ARG, "one of dh_out and dx is required");
+  if (!rstd || !dh) return fail(POET_E_ARG, "null rstd or dh");
+  if (dx && !h_out) return fail(POET_E_ARG, "dx needs h_out");
+  const size_t er = dtype_size(N->res_dtype), ea = dtype_size(N->act_dtype);
+  const int64_t grows = gate ? ((int64_t)N->T + N->gate_tokens - 1) / N->gate_tokens : 0;
+  const NormTensor in[] = {{"h_out", h_out, N->T, N->ldh, er}, {"y", y, N->T, N->ldy, ea}, {"gate", gate, grows, N->ldg, ea},
+                           {"dh_out", dh_out, N->T, N->ldh, er}, {"dx", dx, N->T, N->ldx, ea}};
+  const NormTensor out[] = {{"dh", dh, N->T, N->ldh, er}, {"dy", dy, N->T, N->ldy, ea}, {"dgate", dgate, grows, N->ldg, ea}};
+  for (const auto& t : in) if (!norm_tensor(t, N->d)) return g_last;
+  for (const auto& t : out) if (!norm_tensor(t, N->d)) return g_last;
+  for (const auto& o : out)
+    for (const auto& i : in)
+      if (!(o.p == dh && i.p == dh_out && dh == dh_out) && !norm_apart(o, i, N->d)) return g_last;
+  if (!norm_apart(out[0], out[1], N->d) || !norm_apart(out[0], out[2], N->d) || !norm_apart(out[1], out[2], N->d)) return g_last;
+  if (!check_ws(ws, ws_bytes, poet_block_norm_workspace_bytes(N->T, N->d, gate ? N->gate_tokens : 0))) return g_last;
+  NormArgs a = norm_args(N);
+  a.h = h_out; a.y = y; a.gate = gate; a.w_post = w_post; a.w_pre = w_pre; a.rstd = const_cast<float*>(rstd);
+  a.dh_out = dh_out; a.dx = dx; a.dh = dh; a.dy = dy; a.dgate = dgate; a.dw_post = dw_post; a.dw_pre = dw_pre;
+  Arena ar(ws);
+  HIP_TRY(launch_norm_bwd(a, ar.take_bytes(block_norm_bytes(a.T, a.d, gate ? a.gate_tokens : 0)), st));
+  return POET_OK;
+}
+
 poet_status poet_debug_gemm(const poet_gemm_desc* d, int force_generic, int* used_fast, void* stream) {
   if (!d) return fail(POET_E_ARG, "null descriptor");
   if (d->M < 0 || d->N < 0 || d->K < 0 || d->batch < 0) return fail(POET_E_SHAPE, "negative size");

@@ -1,0 +1,443 @@
+"""GPU tests of the operators on rows of logits (poet_token_logprobs, poet_distill and their backwards) against the
+float64 formulas of tests/token_ref.py, with its bounds: odd and ragged sizes, pitches and misaligned bases, masked
+vocabularies and empty rows, NaN and infinities, ties, absent and repeated entries, in-place gradients, other streams,
+graph replays and offsets past 32 bits."""
+import numpy as np
+import pytest
+
+from tests import token_ref as R
+from tests.gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def B():
+    from orthogonal_reparameterized_amd import binding
+    return binding
+
+
+def tdt(dt):
+    return torch.bfloat16 if dt == "bf16" else torch.float32
+
+
+def rows(a, dt, pad=0, skew=0, fill=None):
+    """A GPU tensor of a's values at pitch V + pad whose base is skew elements into its buffer; (view, float64 values).
+    The buffer around the view holds `fill` (a NaN by default: a read of it would show)."""
+    a = torch.as_tensor(np.asarray(a), dtype=torch.float32)
+    T, V = a.shape
+    buf = torch.full((skew + T * (V + pad),), float("nan") if fill is None else fill, dtype=tdt(dt), device="cuda")
+    v = buf.as_strided((T, V), (V + pad, 1), skew)
+    v.copy_(a)
+    return v, v.double().cpu().numpy(), buf
+
+
+def f32(a):
+    return torch.as_tensor(np.asarray(a), dtype=torch.float32).cuda()
+
+
+def i32(a):
+    return torch.as_tensor(np.asarray(a), dtype=torch.int32).cuda()
+
+
+def close(got, ref, bound, what):
+    got = got.double().cpu().numpy() if isinstance(got, torch.Tensor) else got
+    ref, bound = np.broadcast_arrays(ref, bound)
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    fin = np.isfinite(ref)
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(ref), err_msg=what)
+    inf = ~fin & ~np.isnan(ref)
+    np.testing.assert_array_equal(got[inf], ref[inf], err_msg=what)
+    off = np.abs(got[fin] - ref[fin])
+    bad = off > bound[fin]
+    assert not bad.any(), (what, int(bad.sum()), float(off[bad].max()), float(bound[fin][bad][off[bad].argmax()]))
+
+
+def gauss(T, V, seed, scale=3.0):
+    return np.random.default_rng([T, V, seed]).standard_normal((T, V)) * scale
+
+
+def check_logprobs(zt, z, ids, s=1.0, K=0, gl=None, gh=None, entropy=True, dt="f32", dz=None, ws=None):
+    """One forward (with the gradient when gl or gh is given) against the reference; then the backward by itself."""
+    T, V = z.shape
+    logp, H = torch.full((T,), 7.0, device="cuda"), torch.full((T,), 7.0, device="cuda") if entropy else None
+    stats = torch.full((T, 4), 7.0, device="cuda")
+    ti = torch.full((T, K), -5, dtype=torch.int32, device="cuda") if K else None
+    tl = torch.full((T, K), 7.0, device="cuda") if K else None
+    grads = {}
+    if gl is not None or gh is not None:
+        dz = torch.full((T, V), 7.0, dtype=zt.dtype, device="cuda") if dz is None else dz
+        grads = dict(dlogp=None if gl is None else f32(gl), dentropy=None if gh is None else f32(gh))
+    B().poet_token_logprobs(zt, i32(ids), logp, stats, inv_temp=s, entropy=H, top_ids=ti, top_logp=tl, ws=ws,
+                            dlogits=dz if grads else None, **grads)
+    torch.cuda.synchronize()
+    lp, p, ref_h = R.logprobs(z, s)
+    has = (ids >= 0) & (ids < V)
+    ref = np.where(has, lp[np.arange(T), np.where(has, ids, 0)], 0.0)
+    bound = lambda r: R.DZ + 4 * R.U * np.abs(np.where(np.isfinite(r), r, 0))  # noqa: E731
+    close(logp, ref, bound(ref), "logp")
+    if entropy:
+        close(H, ref_h, R.entropy_bound(z, s), "entropy")
+    if K:
+        at = R.top(z, K)
+        np.testing.assert_array_equal(ti.cpu().numpy(), at)
+        r = np.take_along_axis(lp, at, 1)
+        close(tl, r, bound(r), "top_logp")
+    if grads:
+        ref, err = R.logprobs_grad(z, s, ids, gl, gh)
+        err = err + R.HALF[dt] * np.abs(ref) * 1.01 + 1e-38
+        close(dz, ref, err, "dlogits")
+        again = torch.full((T, V), 3.0, dtype=zt.dtype, device="cuda")
+        if dz.data_ptr() != zt.data_ptr():
+            B().poet_token_logprobs_bwd(zt, i32(ids), stats, grads["dlogp"], again, inv_temp=s, dentropy=grads["dentropy"])
+            torch.cuda.synchronize()
+            close(again, ref, err, "dlogits of the backward")
+    return stats, dz
+
+
+SIZES = [(1, 1), (1, 2), (3, 7), (2, 63), (5, 64), (4, 65), (3, 127), (2, 1000), (3, 2047), (2, 2049), (1, 4099),
+         (2, 8192), (2, 16411), (2, 32000), (3, 33333), (2, 50001), (1, 65537), (1, 131071), (2, 131073), (1, 262147)]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", SIZES)
+def test_logprobs_sizes(T, V, dt):
+    pad, skew = [(0, 0), (1, 0), (3, 1), (0, 5)][V % 4]
+    announce(f"logprobs T={T} V={V} {dt} pad={pad} skew={skew}")
+    zt, z, buf = rows(gauss(T, V, 1), dt, pad, skew)
+    rng = np.random.default_rng(V)
+    ids = rng.integers(0, V, T)
+    check_logprobs(zt, z, ids, K=min(V, 20), dt=dt)
+    check_logprobs(zt, z, ids, s=0.7, K=min(V, 128), gl=rng.standard_normal(T), gh=rng.standard_normal(T), dt=dt)
+    check_logprobs(zt, z, ids, s=2.5, gl=rng.standard_normal(T), entropy=False, dt=dt)
+    check_logprobs(zt, z, ids, gh=rng.standard_normal(T), dt=dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(9, 1001), (300, 4097), (1030, 515)])
+def test_logprobs_many_rows_masks_and_missing_tokens(T, V, dt):
+    announce(f"logprobs masked T={T} V={V} {dt}")
+    rng = np.random.default_rng(T)
+    z = gauss(T, V, 2)
+    z[:, rng.random(V) < 0.7] = -INF
+    z[T // 2] = -INF                                    # a row whose mask leaves nothing
+    z[T // 3, 1:] = -INF                                # a row that it leaves one token
+    z[T // 4] = np.where(rng.random(V) < 0.9, -3.3e38, z[T // 4])  # masked by a lowest value instead
+    z[T - 1] = -3.3e38                                  # ... everywhere: all tokens alike
+    zt, z, _ = rows(z, dt, 3)
+    ids = rng.integers(-1, V + 1, T)
+    ids[0], ids[1] = -100, V
+    check_logprobs(zt, z, ids, K=30, gl=rng.standard_normal(T), gh=rng.standard_normal(T), dt=dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_logprobs_nan_and_infinity(dt):
+    announce(f"logprobs nan {dt}")
+    z = gauss(6, 777, 3)
+    z[0, 5] = np.nan
+    z[1, 700] = INF
+    z[2, :] = -INF
+    z[2, 9] = np.nan
+    z[3, 20] = z[3, 600] = INF
+    z[4, 13] = -INF
+    zt, z, _ = rows(z, dt)
+    T, V = z.shape
+    logp, H, stats = (torch.zeros(T, device="cuda"), torch.zeros(T, device="cuda"), torch.zeros((T, 4), device="cuda"))
+    ti, tl = torch.zeros((T, 9), dtype=torch.int32, device="cuda"), torch.zeros((T, 9), device="cuda")
+    dz = torch.zeros((T, V), dtype=zt.dtype, device="cuda")
+    B().poet_token_logprobs(zt, i32([3, 4, 5, 6, 7, 8]), logp, stats, entropy=H, top_ids=ti, top_logp=tl,
+                            dlogp=f32(np.ones(T)), dlogits=dz)
+    torch.cuda.synchronize()
+    for t in range(4):
+        assert np.isnan(float(logp[t])) and np.isnan(float(H[t])) and tl[t].isnan().all() and dz[t].isnan().all()
+    for t in (4, 5):
+        assert np.isfinite(float(logp[t])) and np.isfinite(float(H[t])) and dz[t].isfinite().all()
+    np.testing.assert_array_equal(ti.cpu().numpy(), R.top(z, 9))
+    # no upstream gradient: zeros, whatever the row holds
+    B().poet_token_logprobs_bwd(zt, i32([-1] * T), stats, f32(np.ones(T)), dz)
+    assert (dz == 0).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["equal", "up", "down", "period", "zeros", "few", "blocks"])
+@pytest.mark.parametrize("V", [1, 100, 2048, 5000, 40961, 140001])
+def test_top_order_of_ties_and_runs(V, kind, dt):
+    """Rows whose best tokens are many equal ones, sit side by side or at one distance from each other."""
+    K = min(V, 33)
+    announce(f"top {kind} V={V} {dt}")
+    j = np.arange(V)
+    z = {"equal": np.full(V, 1.25), "up": np.minimum(j, 30000) * 2.0 ** -7, "down": -np.minimum(j, 30000) * 2.0 ** -7,
+         "period": np.where(j % 2048 < 8, 100.0 + j % 5, 0.0), "zeros": np.where(j % 3 == 0, -0.0, 0.0),
+         "few": np.where(j % 997 == 5, 3.0, -INF), "blocks": (j // 1024 % 7).astype(float)}[kind]
+    zt, z, _ = rows(np.stack([z, z[::-1]]), dt, 1)
+    check_logprobs(zt, z, np.array([0, V - 1]), K=K, dt=dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [999, 33000, 140001])
+def test_gradient_in_place_and_apart(V, dt):
+    """dlogits = logits; and dlogits of another pitch and alignment, whose surroundings stay as they were."""
+    T = 5
+    announce(f"in place V={V} {dt}")
+    rng = np.random.default_rng(V)
+    ids, gl, gh = rng.integers(0, V, T), rng.standard_normal(T), rng.standard_normal(T)
+    zt, z, buf = rows(gauss(T, V, 4), dt, 3, 1, fill=5.0)
+    out = torch.full((T * (V + 6) + 2,), 5.0, dtype=tdt(dt), device="cuda")
+    dz = out.as_strided((T, V), (V + 6, 1), 2)
+    check_logprobs(zt, z, ids, gl=gl, gh=gh, dt=dt, dz=dz)
+    apart = dz.clone()
+    dz.fill_(5.0)
+    assert (out == 5.0).all()
+    check_logprobs(zt, z, ids, gl=gl, gh=gh, dt=dt, dz=zt)
+    assert torch.equal(zt, apart)
+    zt.fill_(5.0)
+    assert (buf == 5.0).all()
+    # the distillation's gradient the same ways
+    zt.copy_(torch.as_tensor(z))
+    t_ids = rng.integers(-1, V, (T, 17))
+    t_z, w = rng.standard_normal((T, 17)), rng.standard_normal(T)
+    loss, stats = torch.empty(T, device="cuda"), torch.empty((T, 4), device="cuda")
+    for mode in (0, 1):
+        zt.copy_(torch.as_tensor(z))
+        lse = f32(np.full(T, 4.0)) if mode else None
+        B().poet_distill(zt, i32(t_ids), f32(t_z), loss, stats, mode=mode, t_lse=lse, dloss=f32(w), dlogits=dz)
+        apart = dz.clone()
+        dz.fill_(5.0)
+        assert (out == 5.0).all()
+        B().poet_distill(zt, i32(t_ids), f32(t_z), loss, stats, mode=mode, t_lse=lse, dloss=f32(w), dlogits=zt)
+        assert torch.equal(zt, apart)
+        zt.copy_(torch.as_tensor(z))
+        B().poet_distill_bwd(zt, i32(t_ids), f32(t_z), stats, f32(w), zt, mode=mode, t_lse=lse)
+        ref, err = R.distill(z, 1.0, t_ids, f32(t_z).double().cpu().numpy(), 1.0, bool(mode),
+                             np.full(T, 4.0) if mode else None, f32(w).double().cpu().numpy())[2:]
+        close(zt, ref, err + R.HALF[dt] * np.abs(ref) * 1.01 + 1e-38, "distill in place")
+        zt.fill_(5.0)
+        assert (buf == 5.0).all()
+
+
+def check_distill(zt, z, t_ids, t_z, s=1.0, ts=1.0, tail=False, lse=None, w=None, dt="f32", ws=None):
+    T, V = z.shape
+    tz, tl = f32(t_z), None if lse is None else f32(lse)
+    loss, stats = torch.full((T,), 7.0, device="cuda"), torch.full((T, 4), 7.0, device="cuda")
+    wd = None if w is None else f32(w)
+    dz = None if w is None else torch.full((T, V), 7.0, dtype=zt.dtype, device="cuda")
+    kw = dict(mode=int(tail), inv_temp=s, t_inv_temp=ts, t_lse=tl)
+    B().poet_distill(zt, i32(t_ids), tz, loss, stats, dloss=wd, dlogits=dz, ws=ws, **kw)
+    torch.cuda.synchronize()
+    ref, err, dref, derr = R.distill(z, s, t_ids, tz.double().cpu().numpy(), float(np.float32(ts)), tail,
+                                     None if lse is None else tl.double().cpu().numpy(),
+                                     None if w is None else wd.double().cpu().numpy())
+    close(loss, ref, err + 2 * R.U * np.abs(np.where(np.isfinite(ref), ref, 0)), "loss")
+    if w is not None:
+        b = derr + R.HALF[dt] * np.abs(dref) * 1.01 + 1e-38
+        close(dz, dref, b, "dlogits")
+        again = torch.full((T, V), 3.0, dtype=zt.dtype, device="cuda")
+        B().poet_distill_bwd(zt, i32(t_ids), tz, stats, wd, again, **kw)
+        torch.cuda.synchronize()
+        close(again, dref, b, "dlogits of the backward")
+    return loss, dz
+
+
+def teacher(z, K, seed):
+    """A teacher near the student: the K best of z plus noise, and the log of its whole sum."""
+    t = z + np.random.default_rng(seed).standard_normal(z.shape)
+    ids = np.argsort(-t, axis=1, kind="stable")[:, :K]
+    m = t.max(1, keepdims=True)
+    return ids, np.take_along_axis(t, ids, 1), (m + np.log(np.exp(t - m).sum(1, keepdims=True)))[:, 0]
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", SIZES)
+def test_distill_sizes(T, V, dt, tail):
+    pad, skew = [(0, 0), (1, 0), (3, 1), (0, 5)][V % 4]
+    K = min(V, 1 + V % 128)
+    announce(f"distill T={T} V={V} K={K} {dt} tail={tail}")
+    zt, z, _ = rows(gauss(T, V, 5), dt, pad, skew)
+    ids, t, lse = teacher(z, K, V)
+    w = np.random.default_rng(V).standard_normal(T)
+    check_distill(zt, z, ids, t, tail=tail, lse=lse if tail else None, w=w, dt=dt)
+    check_distill(zt, z, ids, t, tail=tail, lse=lse if tail else None, dt=dt)
+    ids, t, lse = teacher(z * 0.5, K, V + 1)
+    check_distill(zt, z, ids, t, s=0.5, ts=2.0, tail=tail, lse=2.0 * lse + 0.5 if tail else None, w=w, dt=dt)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [130, 1023, 20001, 140001])
+def test_distill_lists(V, dt, tail):
+    """Absent, repeated and foreign ids, whole rows of them, entries of no mass, masked students, a list that covers
+    the whole vocabulary or leaves tokens of almost no mass, a zero weight."""
+    T, K = 12, 128
+    announce(f"distill lists V={V} {dt} tail={tail}")
+    rng = np.random.default_rng(V)
+    z = gauss(T, V, 6)
+    ids = np.stack([rng.permutation(V)[:K] for _ in range(T)])
+    t = rng.standard_normal((T, K)) - 6.0
+    ids[0, ::3] = -1
+    ids[1] = -1                                   # no teacher
+    ids[2] = rng.integers(0, 4, K)                # repeated ids
+    t[2] -= 1.0
+    ids[3, :5] = [V, V + 7, -100, 2 ** 31 - 1, -2 ** 31]
+    t[4, ::2] = -INF                              # entries of no mass
+    z[5, ids[5]] = -INF                           # the student cannot give them
+    t[5, ::2] = -INF
+    z[6] = -INF                                   # a student row that its mask leaves nothing
+    z[7] -= 200.0                                 # all unlisted tokens far below the listed ones
+    z[7, ids[7]] += 200.0
+    z[8, rng.random(V) < 0.5] = -INF
+    z[8, ids[8]] = 1.0
+    ids[9, 1:] = -1                               # one entry
+    t[9, 0] = -0.001 if tail else 3.0
+    t[10] = -INF                                  # a list without mass
+    if not tail:
+        t[10, 3] = 0.0
+    zt, z, _ = rows(z, dt, 1)
+    w = rng.standard_normal(T)
+    w[11] = 0.0
+    check_distill(zt, z, ids, t, tail=tail, w=w, dt=dt)
+    if V == 130 and tail:                         # the list covers every token: nothing is left on either side
+        full = np.tile(np.arange(V)[:K], (T, 1))
+        z2 = z.copy()
+        z2[:, K:] = -INF
+        z2[5:7] = gauss(2, V, 8)
+        z2[5:7, K:] = -INF
+        zt2, z2, _ = rows(z2, dt)
+        lq, _, _ = R.logprobs(gauss(T, K, 9))
+        check_distill(zt2, z2, full, lq + 1e-3, tail=True, w=w, dt=dt)
+
+
+def test_gradients_against_differences():
+    """Both gradients against central differences of the float64 formulas along random directions."""
+    T, V, K, s, e = 4, 61, 9, 0.8, 1e-5
+    announce("gradients against differences")
+    rng = np.random.default_rng(0)
+    zt, z, _ = rows(gauss(T, V, 7), "f32")
+    ids, gl, gh = rng.integers(0, V, T), rng.standard_normal(T), rng.standard_normal(T)
+    gl, gh = np.float32(gl).astype(float), np.float32(gh).astype(float)
+    _, dz = check_logprobs(zt, z, ids, s=s, gl=gl, gh=gh)
+
+    def value(x):
+        lp, _, H = R.logprobs(x, s)
+        return (gl * lp[np.arange(T), ids]).sum() + (gh * H).sum()
+    t_ids, t_z, lse = teacher(z, K, 1)
+    t_z, lse = np.float32(t_z).astype(float), np.float32(lse + 0.3).astype(float)
+    for tail in (None, False, True):
+        if tail is not None:
+            _, dz = check_distill(zt, z, t_ids, t_z, s=s, tail=tail, lse=lse if tail else None, w=gl)
+            value = lambda x: (gl * R.distill(x, s, t_ids, t_z, 1.0, tail, lse if tail else None)[0]).sum()  # noqa: E731,B023
+        g = dz.double().cpu().numpy()
+        for r in range(3):
+            u = np.random.default_rng(r).standard_normal((T, V))
+            diff = (value(z + e * u) - value(z - e * u)) / (2 * e)
+            # second-order term of the difference: e^2 times a third derivative of order 1; rounding 1e-16 / e
+            assert abs((g * u).sum() - diff) <= 2e-5 * (np.abs(g * u).sum() + 1.0), (tail, r)
+
+
+def test_offsets_past_32_bits():
+    """Row offsets beyond 2^31 elements and 2^32 bytes."""
+    T, V, ld = 3, 1000, 1_200_000_008
+    announce("offsets past 32 bits")
+    buf = torch.empty((T - 1) * ld + V, dtype=torch.bfloat16, device="cuda")
+    zt = buf.as_strided((T, V), (ld, 1), 0)
+    zt.copy_(torch.as_tensor(gauss(T, V, 10)))
+    z = zt.double().cpu().numpy()
+    ids = np.array([1, 2, 999])
+    rng = np.random.default_rng(1)
+    check_logprobs(zt, z, ids, K=5, gl=rng.standard_normal(T), gh=rng.standard_normal(T), dt="bf16", dz=zt)
+    zt.copy_(torch.as_tensor(z))
+    t_ids, t_z, lse = teacher(z, 8, 2)
+    check_distill(zt, z, t_ids, t_z, tail=True, lse=lse, w=rng.standard_normal(T), dt="bf16")
+
+
+def test_empty_batch():
+    z = torch.empty((0, 50), device="cuda")
+    e, st = torch.empty(0, device="cuda"), torch.empty((0, 4), device="cuda")
+    i = torch.empty(0, dtype=torch.int32, device="cuda")
+    B().poet_token_logprobs(z, i, e, st, entropy=e, dlogp=e, dlogits=torch.empty_like(z))
+    B().poet_token_logprobs_bwd(z, i, st, e, torch.empty_like(z))
+    ti, tz = torch.empty((0, 4), dtype=torch.int32, device="cuda"), torch.empty((0, 4), device="cuda")
+    B().poet_distill(z, ti, tz, e, st, dloss=e, dlogits=torch.empty_like(z))
+    B().poet_distill_bwd(z, ti, tz, st, e, torch.empty_like(z))
+    torch.cuda.synchronize()
+
+
+def test_rows_behind_the_last_stay():
+    """Outputs larger rows would fall into are left alone: the rows after T of every output buffer."""
+    T, V, K = 3, 4097, 6
+    announce("rows behind the last")
+    big = torch.full((T + 2, V), 9.0, device="cuda")
+    z = torch.randn((T, V), device="cuda")
+    lg, H = torch.full((T + 2,), 9.0, device="cuda"), torch.full((T + 2,), 9.0, device="cuda")
+    st, tl = torch.full((T + 2, 4), 9.0, device="cuda"), torch.full((T + 2, K), 9.0, device="cuda")
+    ti = torch.full((T + 2, K), 9, dtype=torch.int32, device="cuda")
+    B().poet_token_logprobs(z, i32([1, 2, 3]), lg[:T], st[:T], entropy=H[:T], top_ids=ti[:T], top_logp=tl[:T],
+                            dlogp=f32([1, 1, 1]), dlogits=big[:T])
+    B().poet_distill(z, ti[:T], tl[:T], lg[:T], st[:T], dloss=f32([1, 1, 1]), dlogits=big[:T])
+    for t in (big, lg, H, st, tl, ti):
+        assert (t[T:] == 9).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(1, 140001), (700, 3001), (3, 32000)])
+def test_two_streams_and_graph_replay(T, V, dt):
+    """The same calls on two streams at once (each with its own workspace and outputs) and replayed from a graph with
+    eager work between the replays: the same bits every time."""
+    announce(f"streams and graph T={T} V={V} {dt}")
+    K = 10
+    zt, z, _ = rows(gauss(T, V, 11), dt, 1)
+    ids = i32(np.random.default_rng(0).integers(0, V, T))
+    one = torch.ones(T, device="cuda")
+    dtc = B().POET_BF16 if dt == "bf16" else B().POET_F32
+    need = max(B().poet_token_logprobs_workspace_bytes(T, V, dtc, K), B().poet_distill_workspace_bytes(T, V, dtc), 1)
+
+    def outs():
+        o = dict(logp=torch.empty(T, device="cuda"), stats=torch.empty((T, 4), device="cuda"),
+                 entropy=torch.empty(T, device="cuda"), top_ids=torch.empty((T, K), dtype=torch.int32, device="cuda"),
+                 top_logp=torch.empty((T, K), device="cuda"), dlogits=torch.empty((T, V), dtype=zt.dtype, device="cuda"))
+        d = dict(loss=torch.empty(T, device="cuda"), stats=torch.empty((T, 4), device="cuda"),
+                 dlogits=torch.empty((T, V), dtype=zt.dtype, device="cuda"))
+        return o, d, torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def call(bufs, stream=None):
+        o, d, ws = bufs
+        B().poet_token_logprobs(zt, ids, dlogp=one, dentropy=one, ws=ws, stream=stream, **o)
+        B().poet_distill(zt, o["top_ids"], o["top_logp"], mode=1, dloss=one, ws=ws, stream=stream, **d)
+
+    def flat(bufs):
+        return [t.clone() for part in bufs[:2] for t in part.values()]
+    ref = outs()
+    call(ref)
+    want = flat(ref)
+    streams, bufs = [torch.cuda.Stream(), torch.cuda.Stream()], [outs(), outs()]
+    torch.cuda.synchronize()
+    for s, b in zip(streams, bufs):
+        call(b, s)
+    torch.cuda.synchronize()
+    for b in bufs:
+        assert all(torch.equal(x, y) for x, y in zip(want, flat(b)))
+    b = outs()
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call(b)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        call(b)
+    for _ in range(3):
+        for part in b[:2]:
+            for t in part.values():
+                t.fill_(3)
+        call(ref)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, flat(b)))
