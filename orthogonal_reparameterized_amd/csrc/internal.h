@@ -314,9 +314,15 @@ struct TokenArgs {
   float* stats = nullptr;
   void* dz = nullptr; int64_t ldd = 0;
 };
-hipError_t launch_logprobs(const TokenArgs& a, hipStream_t st);
+// Rows in nseg segments of len elements (1: whole rows): segment q of row t leaves its partials at part + (t nseg + q)
+// stride floats; a segment is `steps` 16-byte steps at most.
+struct RowSplit { int nseg = 1, len = 0, stride = 0, steps = 0; float* part = nullptr; };
+// scratch of the launches below (0 where a workgroup holds a row, however it is aligned)
+size_t logprobs_part_bytes(int T, int V, int dt, int K);
+size_t distill_part_bytes(int T, int V, int dt);
+hipError_t launch_logprobs(const TokenArgs& a, float* part, hipStream_t st);      // and the gradient where a.dz is set
 hipError_t launch_logprobs_bwd(const TokenArgs& a, hipStream_t st);
-hipError_t launch_distill(const TokenArgs& a, hipStream_t st);
+hipError_t launch_distill(const TokenArgs& a, float* part, hipStream_t st);       // and the gradient where a.dz is set
 hipError_t launch_distill_bwd(const TokenArgs& a, hipStream_t st);
 
 // The seam between two blocks of linears (block_norm.hip), fields as the arguments of poet_block_norm_fwd / _bwd (h in

@@ -2267,7 +2267,8 @@ size_t poet_token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t dtype, 
   const poet_logits L{T, V, V, dtype, 1.f};
   if (!logits_info(&L)) return 0;
   if (K < 0 || K > V || K > POET_MAX_TOP) return fail(POET_E_SHAPE, "K = %d for V = %d (at most %d)", K, V, POET_MAX_TOP), 0;
-  return 0;
+  const size_t b = logprobs_part_bytes(T, V, dtype, K);
+  return b ? b + 256 : 0;
 }
 
 poet_status poet_token_logprobs(const poet_logits* L, const void* logits, const int32_t* ids, int32_t K,
@@ -2290,8 +2291,8 @@ poet_status poet_token_logprobs(const poet_logits* L, const void* logits, const 
   TokenArgs a = token_args(L, logits);
   a.ids = ids; a.K = K; a.dlogp = dlogp; a.dentropy = dentropy; a.logp = logp; a.entropy = entropy;
   a.top_ids = top_ids; a.top_logp = top_logp; a.stats = stats; a.dz = dlogits; a.ldd = ldd;
-  HIP_TRY(launch_logprobs(a, st));
-  if (dlogits) HIP_TRY(launch_logprobs_bwd(a, st));
+  Arena ar(ws);
+  HIP_TRY(launch_logprobs(a, ar.take<float>(0), st));
   return POET_OK;
 }
 
@@ -2322,7 +2323,8 @@ static bool teacher_info(const poet_teacher* t, const float* t_lse) {
 size_t poet_distill_workspace_bytes(int32_t T, int32_t V, int32_t dtype) {
   const poet_logits L{T, V, V, dtype, 1.f};
   if (!logits_info(&L)) return 0;
-  return 0;
+  const size_t b = distill_part_bytes(T, V, dtype);
+  return b ? b + 256 : 0;
 }
 
 poet_status poet_distill(const poet_logits* L, const poet_teacher* teacher, const void* logits, const int32_t* t_ids,
@@ -2338,8 +2340,8 @@ poet_status poet_distill(const poet_logits* L, const poet_teacher* teacher, cons
   TokenArgs a = token_args(L, logits);
   a.K = teacher->K; a.t_ids = t_ids; a.t_z = t_logits; a.t_lse = t_lse; a.tail = teacher->mode == POET_DISTILL_TAIL;
   a.ts = teacher->inv_temp; a.dloss = dloss; a.loss = loss; a.stats = stats; a.dz = dlogits; a.ldd = ldd;
-  HIP_TRY(launch_distill(a, st));
-  if (dlogits) HIP_TRY(launch_distill_bwd(a, st));
+  Arena ar(ws);
+  HIP_TRY(launch_distill(a, ar.take<float>(0), st));
   return POET_OK;
 }
 

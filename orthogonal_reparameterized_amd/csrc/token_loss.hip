@@ -1,8 +1,12 @@
 // What a model's last linear answers with: log-probabilities of given tokens with the entropy and the best
 // alternatives of each row of logits, the distillation loss on a teacher's top logits, and the gradients of both.
 //
-// With z a row of V logits, s = inv_temp, m = max z, d = (z - m) s, Z = sum exp d:
-//   log p_j = d_j - log Z,   entropy H = log Z - (1/Z) sum exp(d) d   (both sums have one sign: nothing cancels).
+// With z a row of V logits, s = inv_temp, m = max z, d = z - m, Z = sum exp(s d):
+//   log p_j = s d_j - log Z,   entropy H = log Z - (s/Z) sum exp(s d) d   (both sums have one sign: nothing cancels).
+// Both operators and their gradients are bound by HBM: a row is read once (and its gradient written once), so one
+// workgroup keeps a whole row in registers, 16 bytes a thread and step, and every pass over it (maximum, sums, best
+// alternatives, gradient) reads those. Rows beyond a workgroup's registers are split into segments whose maxima, sums
+// and best alternatives a second launch joins; their gradient is a launch of its own.
 #include <algorithm>
 #include <cmath>
 
@@ -12,18 +16,91 @@
 namespace poet {
 namespace {
 
-constexpr int kThreads = 256;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr float kLow = -1.0e30f;  // stands in for -inf where it would meet a zero factor, and survives a gradient times it
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kMaxBlocks = 1 << 20;  // workgroups of one launch; they stride over the rest
+constexpr int kCand = 512;           // candidates for the best alternatives that one workgroup keeps
 
-template <class T> __device__ __forceinline__ float ld(const T* p, int64_t i) { return (float)p[i]; }
-template <class T> __device__ __forceinline__ void st(T* p, int64_t i, float v) { p[i] = (T)v; }
-
-__device__ __forceinline__ float wave_max(float v) {
+// ---- 16-byte steps of a row ----------------------------------------------------------------------------------
+// A row of n elements is up to N-1 elements before the first 16-byte boundary, steps of N elements from there, and up to
+// N-1 elements behind the last step. A thread holds some steps and, where it is one of the first few, one of the single
+// elements, so that any alignment and pitch goes at full speed and nothing outside the row is touched.
+template <class T> struct Vec;
+template <> struct Vec<__bf16> {
+  static constexpr int N = 8;
+  static constexpr uint32_t kNone = 0xff80ff80u;  // -inf in every element
+  static __device__ __forceinline__ float get(const u32x4& v, int k) {
+    const uint32_t w = v[k >> 1];
+    return __uint_as_float(k & 1 ? w & 0xffff0000u : w << 16);
+  }
+  static __device__ __forceinline__ void none(u32x4& v, int k) {
+    v[k >> 1] = k & 1 ? (v[k >> 1] & 0xffffu) | 0xff800000u : (v[k >> 1] & 0xffff0000u) | 0xff80u;
+  }
+  // one rounding to nearest even of the float32 result
+  static __device__ __forceinline__ u32x4 pack(const float* f) {
+    u32x4 r;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+    for (int k = 0; k < 4; ++k) {
+      typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+      typedef float f2 __attribute__((ext_vector_type(2)));
+      const f2 x = {f[2 * k], f[2 * k + 1]};
+      r[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, b2));
+    }
+    return r;
+  }
+};
+template <> struct Vec<float> {
+  static constexpr int N = 4;
+  static constexpr uint32_t kNone = 0xff800000u;
+  static __device__ __forceinline__ float get(const u32x4& v, int k) { return __uint_as_float(v[k]); }
+  static __device__ __forceinline__ void none(u32x4& v, int k) { v[k] = kNone; }
+  static __device__ __forceinline__ u32x4 pack(const float* f) {
+    return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+  }
+};
+
+template <class T> struct Steps {
+  static constexpr int N = Vec<T>::N;
+  const T* p;        // the row's first element
+  int head, steps, singles;  // elements before the steps; the steps; single elements before and behind them
+  __device__ Steps(const T* row, int n) : p(row) {
+    const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    head = lead ? min(n, N - lead) : 0;
+    steps = (n - head) / N;
+    singles = n - steps * N;
+  }
+  __device__ __forceinline__ int first(int v) const { return head + v * N; }  // the row's index of a step's element 0
+  __device__ __forceinline__ int single(int e) const { return e < head ? e : e + steps * N; }  // ... of single element e
+  // a uniform base and an unsigned 32-bit offset: one address register a step
+  __device__ __forceinline__ u32x4 load(int v) const {
+    return *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(p + head) + (uint32_t)v * 16u);
+  }
+  __device__ __forceinline__ void store(T* out, int v, const float* f) const {  // out: aligned like the row
+    *reinterpret_cast<u32x4*>(reinterpret_cast<char*>(out + head) + (uint32_t)v * 16u) = Vec<T>::pack(f);
+  }
+};
+
+// ---- reductions ------------------------------------------------------------------------------------------------
+template <int CTRL, int ROWS> __device__ __forceinline__ float dpp(float old, float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, ROWS, 0xf, false));
 }
-template <class A> __device__ __forceinline__ A wave_sum(A v) {
+// the result of all 64 lanes in every lane; every lane is active
+template <class F> __device__ __forceinline__ float wave_all(float v, float id, F f) {
+  v = f(v, dpp<0x111, 0xf>(id, v));  // row_shr 1, 2, 4, 8: lane 15 of each row of 16 holds the row's
+  v = f(v, dpp<0x112, 0xf>(id, v));
+  v = f(v, dpp<0x114, 0xf>(id, v));
+  v = f(v, dpp<0x118, 0xf>(id, v));
+  v = f(v, dpp<0x142, 0xa>(id, v));  // row_bcast 15, 31
+  v = f(v, dpp<0x143, 0xc>(id, v));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ float fadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float fmax2(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float wave_sum(float v) { return wave_all(v, 0.f, fadd); }
+__device__ __forceinline__ float wave_max(float v) { return wave_all(v, -INFINITY, fmax2); }
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
@@ -36,212 +113,758 @@ __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
   }
   return v;
 }
-
-// every thread gets the block's result; red holds one entry per wave, free again after the call
-template <class A, class F> __device__ __forceinline__ A block_all(A v, A* red, F f) {
-  const int w = threadIdx.x >> 6, n = blockDim.x >> 6;
-  if ((threadIdx.x & 63) == 0) red[w] = v;
-  __syncthreads();
-  A r = red[0];
-  for (int i = 1; i < n; ++i) r = f(r, red[i]);
-  __syncthreads();
+// orders this wave's own LDS accesses across its lanes
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+// the three-way maximum as one instruction: the compiler's own form quiets every operand first
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
   return r;
 }
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// order of the alternatives: larger logit first, then the lower index; NaN after everything else
+// ---- the order of the alternatives ----------------------------------------------------------------------------
+// larger logit first, then the lower index; NaN after everything else (o = 0). Keys of one row are distinct.
+__device__ __forceinline__ uint32_t ordered(float z) {
+  const uint32_t b = __float_as_uint(z + 0.f);  // -0 and +0 are equal
+  return b ^ (uint32_t)((int32_t)b >> 31 | (int32_t)0x80000000);
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float(o >> 31 ? o ^ 0x80000000u : ~o);
+}
 __device__ __forceinline__ uint64_t rank_key(float z, int j) {
-  z += 0.f;  // -0 and +0 are equal
-  const uint32_t b = __float_as_uint(z);
-  const uint32_t o = z != z ? 0u : (b >> 31 ? ~b : b | 0x80000000u);
-  return ((uint64_t)o << 32) | (uint32_t)~j;
+  return (uint64_t)(z != z ? 0u : ordered(z)) << 32 | (uint32_t)~j;
 }
 
-template <class T>
-__global__ __launch_bounds__(kThreads) void k_logprobs(const TokenArgs a) {
-  __shared__ double rd[kThreads / 64];
-  __shared__ float rf[kThreads / 64];
-  __shared__ uint64_t rk[kThreads / 64];
-  const int row = blockIdx.x;
-  const T* z = (const T*)a.z + row * a.ld;
-  float m = -INFINITY;
-  for (int j = threadIdx.x; j < a.V; j += kThreads) m = fmaxf(m, ld(z, j));
-  m = block_all(wave_max(m), rf, [](float x, float y) { return fmaxf(x, y); });
-  const bool empty = m == -INFINITY;
-  const float ref = empty ? 0.f : m;
-  double Z = 0, S = 0;
-  for (int j = threadIdx.x; j < a.V; j += kThreads) {
-    const float d = (ld(z, j) - ref) * a.s, e = expf(d);
-    Z += e;
-    S += e * fmaxf(d, kLow);
-  }
-  const auto add = [](double x, double y) { return x + y; };
-  Z = block_all(wave_sum(Z), rd, add);
-  S = block_all(wave_sum(S), rd, add);
-  const bool none = empty && Z == 0.0;  // every logit is -inf (a NaN would be in Z)
-  const float logZ = (float)log(Z), H = none ? 0.f : (float)(log(Z) - S / Z);
-  uint64_t last = ~0ull;
-  for (int k = 0; k < a.K; ++k) {
-    uint64_t best = 0;
-    for (int j = threadIdx.x; j < a.V; j += kThreads) {
-      const uint64_t q = rank_key(ld(z, j), j);
-      if (q < last && q > best) best = q;
+// ---- one row or segment in registers ---------------------------------------------------------------------------
+template <class T, int NT, int VPT> struct Held {
+  u32x4 d[VPT];  // step threadIdx.x + i NT; -inf where there is none
+  float x;       // single element threadIdx.x; -inf where there is none
+  __device__ __forceinline__ void load(const Steps<T>& s) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = threadIdx.x + i * NT;
+      d[i][0] = d[i][1] = d[i][2] = d[i][3] = Vec<T>::kNone;
+      if (v < s.steps) d[i] = s.load(v);
     }
-    last = block_all(wave_max64(best), rk, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
-    const int j = (int)~(uint32_t)last;
-    if (threadIdx.x == 0) {
-      a.top_ids[(int64_t)row * a.K + k] = j;
-      a.top_logp[(int64_t)row * a.K + k] = none ? -INFINITY : (ld(z, j) - ref) * a.s - logZ;
-    }
+    x = (int)threadIdx.x < s.singles ? (float)s.p[s.single(threadIdx.x)] : -INFINITY;
   }
-  if (threadIdx.x) return;
-  float* q = a.stats + (int64_t)row * 4;
-  q[0] = m; q[1] = logZ; q[2] = H; q[3] = 0.f;
-  if (a.entropy) a.entropy[row] = H;
-  if (a.logp) {
-    const int id = a.ids[row];
-    a.logp[row] = id < 0 || id >= a.V ? 0.f : none ? -INFINITY : (ld(z, id) - ref) * a.s - logZ;
+  // Between two passes: without it the compiler keeps what one pass unpacked for the next (twice the registers for bf16,
+  // spilled to memory) instead of unpacking again, one instruction an element.
+  __device__ __forceinline__ void repack() {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) asm volatile("" : "+v"(d[i]));
   }
-}
-
-template <class T>
-__global__ __launch_bounds__(kThreads) void k_logprobs_bwd(const TokenArgs a) {
-  const int row = blockIdx.x;
-  const T* z = (const T*)a.z + row * a.ld;
-  T* dz = (T*)a.dz + row * a.ldd;
-  const float m = a.stats[(int64_t)row * 4], logZ = a.stats[(int64_t)row * 4 + 1], H = a.stats[(int64_t)row * 4 + 2];
-  const int id = a.ids && a.dlogp ? a.ids[row] : -1;
-  const float gl = id < 0 || id >= a.V ? 0.f : a.dlogp[row], gh = a.dentropy ? a.dentropy[row] : 0.f;
-  const bool none = m == -INFINITY && logZ == -INFINITY, zero = none || (gl == 0.f && gh == 0.f);
-  const float ref = m == -INFINITY ? 0.f : m;
-  for (int j = threadIdx.x; j < a.V; j += kThreads) {
-    float g = 0.f;
-    if (!zero) {
-      const float lp = (ld(z, j) - ref) * a.s - logZ, p = expf(lp);
-      g = -p * (gl + gh * (fmaxf(lp, kLow) + H));
-      if (j == id) g += gl;
-    }
-    st(dz, j, g * a.s);
+  __device__ __forceinline__ float max() const {
+    float m = x;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int k = 0; k < Vec<T>::N; k += 2) m = max3(m, Vec<T>::get(d[i], k), Vec<T>::get(d[i], k + 1));
+    return m;
   }
-}
-
-// The teacher's list of one row: q[k] = its probability of entry k (0 for absent ones), log q[k], id[k] (-1 absent).
-struct List {
-  float q[POET_MAX_TOP], lq[POET_MAX_TOP], z[POET_MAX_TOP];
-  int id[POET_MAX_TOP];
-  float qt;   // TAIL: what the list leaves
-  int some;   // any entry present
 };
 
-template <class T>
-__device__ void load_list(List& L, const TokenArgs& a, int row, const T* z) {
-  for (int k = threadIdx.x; k < a.K; k += kThreads) {
-    int id = a.t_ids[(int64_t)row * a.K + k];
+template <int NT> struct Shared {
+  float m[NT / 64], z[NT / 64], s[NT / 64];
+  float tmax[NT];           // each thread's largest logit
+  uint64_t cand[kCand];
+  uint16_t win[NT];         // threads that can hold one of the best
+  uint64_t best[NT / 64];
+  float tau;
+  int nwin, ncand;
+};
+
+// The K best alternatives of a row or segment, ranked, as out(rank, key).
+// Threads' own maxima bound them: with tau the K-th largest of those, K elements are >= tau, and an element >= tau sits
+// with a thread whose maximum is >= tau. One wave finds tau bit by bit and lists those threads, a little over K of them;
+// the waves read the elements of one listed thread at a time again (from the cache: 64 lanes side by side, where a scan
+// of the registers would cost every wave all its steps), and the few >= tau are ranked against each other. Rows where
+// that is not few (many ties, fewer threads with logits than K), or that hold a NaN, are read again K times.
+template <class T, int NT, int VPT, class Out>
+__device__ void best_of(const Steps<T>& s, int base, int n, int K, float tmax, bool sure,
+                        Shared<NT>& sh, Out out) {
+  constexpr int N = Vec<T>::N;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (sure) {  // uniform
+    sh.tmax[tid] = tmax;
+    __syncthreads();
+    if (wave == 0) {
+      uint32_t key[NT / 64], t = 0;
+#pragma unroll
+      for (int q = 0; q < NT / 64; ++q) key[q] = ordered(sh.tmax[q * 64 + lane]);
+      // bf16 logits differ in the upper 16 bits only; 10 bits less than float32's 32 let in a few threads more
+      for (int bit = 31; bit >= (N == 8 ? 16 : 10); --bit) {
+        const uint32_t c = t | 1u << bit;
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < NT / 64; ++q) n += __popcll(__ballot(key[q] >= c));
+        if (n >= K) t = c;
+        if (n == K) break;
+      }
+      int n = 0;
+#pragma unroll
+      for (int q = 0; q < NT / 64; ++q) {
+        const uint64_t b = __ballot(key[q] >= t);
+        if (key[q] >= t) sh.win[n + __popcll(b & ((1ull << lane) - 1))] = (uint16_t)(q * 64 + lane);
+        n += __popcll(b);
+      }
+      if (lane == 0) { sh.nwin = n; sh.ncand = 0; sh.tau = unordered(t); }
+    }
+    __syncthreads();
+    const float tau = sh.tau;
+    const int nwin = sh.nwin;
+    sure = tau > -INFINITY && nwin <= 2 * K + 64;
+    if (sure) {
+      for (int w = wave; w < nwin; w += NT / 64) {
+        const int v0 = sh.win[w];
+#pragma unroll
+        for (int t0 = 0; t0 < VPT * N + 1; t0 += 64) {
+          const int t = t0 + lane, v = v0 + t / N * NT;  // element t of the thread's, the last one its single element
+          const bool step = t < VPT * N && v < s.steps, single = t == VPT * N && v0 < s.singles;
+          if (step || single) {
+            const int j = step ? s.first(v) + t % N : s.single(v0);
+            const float z = (float)s.p[j];
+            if (z >= tau) {
+              const int c = atomicAdd(&sh.ncand, 1);
+              if (c < kCand) sh.cand[c] = rank_key(z, base + j);
+            }
+          }
+        }
+      }
+      __syncthreads();
+      const int nc = sh.ncand;
+      sure = nc >= K && nc <= kCand;
+      if (sure) {
+        for (int c = tid; c < nc; c += NT) {
+          const uint64_t key = sh.cand[c];
+          int rank = 0;
+          for (int o = 0; o < nc; ++o) rank += sh.cand[o] > key;
+          if (rank < K) out(rank, key);
+        }
+      }
+    }
+  }
+  if (sure) return;
+  uint64_t last = ~0ull;
+  for (int k = 0; k < K; ++k) {
+    uint64_t best = 0;
+    for (int j = tid; j < n; j += NT) {
+      const uint64_t q = rank_key((float)s.p[j], base + j);
+      if (q < last && q > best) best = q;
+    }
+    best = wave_max64(best);
+    __syncthreads();  // the round before has read them
+    if (lane == 0) sh.best[wave] = best;
+    __syncthreads();
+    last = sh.best[0];
+#pragma unroll
+    for (int q = 1; q < NT / 64; ++q) last = sh.best[q] > last ? sh.best[q] : last;
+    if (tid == 0) out(k, last);
+  }
+}
+
+// ---- log-probabilities --------------------------------------------------------------------------------------------
+// a row's results from its maximum m, Z = sum exp(s (z - m)) and S = sum exp(s (z - m)) (z - m)
+struct RowStat {
+  float m, ref, logZ, H;
+  bool none;  // every logit is -inf (a NaN would be in Z)
+  __device__ RowStat(float m_, float Z, float S, float s) {
+    m = m_;
+    none = m == -INFINITY && Z == 0.f;
+    ref = m == -INFINITY ? 0.f : m;
+    logZ = logf(Z);
+    H = none ? 0.f : logZ - s * S / Z;
+  }
+  __device__ __forceinline__ float logp(float z, float s) const { return none ? -INFINITY : (z - ref) * s - logZ; }
+};
+
+__device__ __forceinline__ int token_of(const TokenArgs& a, int64_t row) {
+  const int id = a.ids ? a.ids[row] : -1;
+  return id >= 0 && id < a.V ? id : -1;
+}
+
+__device__ void write_row(const TokenArgs& a, int64_t row, const RowStat& r, float z_id, int id) {
+  float* q = a.stats + row * 4;
+  q[0] = r.m; q[1] = r.logZ; q[2] = r.H; q[3] = 0.f;
+  if (a.entropy) a.entropy[row] = r.H;
+  if (a.logp) a.logp[row] = id < 0 ? 0.f : r.logp(z_id, a.s);
+}
+
+// The gradient of one row's logits is e (A + B d) with e = exp(s d), d = z - m, plus gl s at the token:
+//   dz = s (gl (delta - p) - gh p (log p + H)),  p = e / Z,  log p = s d - log Z.
+struct RowGrad {
+  float c, ref, A, B, gl;
+  int id;
+  bool zero;
+  __device__ RowGrad(const TokenArgs& a, int64_t row, int tok, float m, float logZ, float H) {
+    id = a.dlogp ? tok : -1;
+    gl = id < 0 ? 0.f : a.dlogp[row];
+    const float gh = a.dentropy ? a.dentropy[row] : 0.f;
+    zero = (gl == 0.f && gh == 0.f) || (m == -INFINITY && logZ == -INFINITY);
+    ref = m == -INFINITY ? 0.f : m;
+    c = a.s * kLog2e;
+    const float inv = expf(-logZ) * a.s;
+    A = -inv * (gl + gh * (H - logZ));
+    B = -inv * gh * a.s;
+    gl *= a.s;
+  }
+  __device__ __forceinline__ float one(float z, int j) const {
+    const float d = z - ref;
+    return zero ? 0.f : exp2_fast(d * c) * fmaf(B, fmaxf(d, kLow), A) + (j == id ? gl : 0.f);
+  }
+  template <class T> __device__ __forceinline__ void step(const u32x4& v, int j0, float* f) const {
+#pragma unroll
+    for (int k = 0; k < Vec<T>::N; ++k) {
+      const float d = Vec<T>::get(v, k) - ref;
+      f[k] = exp2_fast(d * c) * fmaf(B, fmaxf(d, kLow), A);
+    }
+    if ((unsigned)(id - j0) < (unsigned)Vec<T>::N) {
+#pragma unroll
+      for (int k = 0; k < Vec<T>::N; ++k)
+        if (j0 + k == id) f[k] += gl;
+    }
+    if (zero) {
+#pragma unroll
+      for (int k = 0; k < Vec<T>::N; ++k) f[k] = 0.f;
+    }
+  }
+};
+
+// One workgroup a row (nseg == 1: results, and the gradient where asked) or a segment of a row (partials into `part`:
+// m, Z, S, -, then the K best keys).
+template <class T, int NT, int VPT>
+__global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const RowSplit sp) {
+  __shared__ Shared<NT> sh;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  for (int64_t w = blockIdx.x; w < (int64_t)a.T * sp.nseg; w += gridDim.x) {
+    const int64_t row = sp.nseg == 1 ? w : w / sp.nseg;
+    const int seg = sp.nseg == 1 ? 0 : (int)(w - row * sp.nseg);
+    const int base = seg * sp.len;
+    const T* z = (const T*)a.z + row * a.ld;
+    const int n = min(sp.len, a.V - base);
+    const Steps<T> s(z + base, n);
+    Held<T, NT, VPT> h;
+    h.load(s);
+    const int id = sp.nseg == 1 ? token_of(a, row) : -1;
+    const float z_id = id >= 0 ? (float)z[id] : 0.f;  // before the gradient may overwrite it
+    const float tmax = h.max();
+    float m = wave_max(tmax);
+    if (lane == 0) sh.m[wave] = m;
+    __syncthreads();
+    m = sh.m[0];
+#pragma unroll
+    for (int q = 1; q < NT / 64; ++q) m = fmaxf(m, sh.m[q]);
+    const float ref = m == -INFINITY ? 0.f : m, c = a.s * kLog2e;
+    float Z = 0.f, S = 0.f;
+    h.repack();
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float zi = 0.f, si = 0.f;
+#pragma unroll
+      for (int k = 0; k < Vec<T>::N; ++k) {
+        const float d = Vec<T>::get(h.d[i], k) - ref, e = exp2_fast(d * c);
+        zi += e;
+        si = fmaf(e, fmaxf(d, kLow), si);
+      }
+      Z += zi;
+      S += si;
+    }
+    {
+      const float d = h.x - ref, e = exp2_fast(d * c);
+      Z += e;
+      S = fmaf(e, fmaxf(d, kLow), S);
+    }
+    Z = wave_sum(Z);
+    S = wave_sum(S);
+    if (lane == 0) { sh.z[wave] = Z; sh.s[wave] = S; }
+    __syncthreads();
+    Z = sh.z[0];
+    S = sh.s[0];
+#pragma unroll
+    for (int q = 1; q < NT / 64; ++q) { Z += sh.z[q]; S += sh.s[q]; }
+    const RowStat r(m, Z, S, a.s);
+    if (sp.nseg > 1) {
+      float* p = sp.part + w * sp.stride;
+      if (tid == 0) { p[0] = m; p[1] = Z; p[2] = S; }
+      const int K = min(a.K, n);
+      if (K > 0)
+        best_of<T, NT, VPT>(s, base, n, K, tmax, Z == Z, sh,
+                            [&](int k, uint64_t key) { reinterpret_cast<uint64_t*>(p + 4)[k] = key; });
+      for (int k = K + tid; k < a.K; k += NT) reinterpret_cast<uint64_t*>(p + 4)[k] = 0;  // a short last segment
+      __syncthreads();
+      continue;
+    }
+    if (tid == 0) write_row(a, row, r, z_id, id);
+    if (a.K > 0)
+      best_of<T, NT, VPT>(s, 0, n, a.K, tmax, Z == Z, sh, [&](int k, uint64_t key) {
+        a.top_ids[row * a.K + k] = (int)~(uint32_t)key;
+        a.top_logp[row * a.K + k] = r.logp(unordered((uint32_t)(key >> 32)), a.s);
+      });
+    if (a.dz) {
+      if (a.K > 0) __syncthreads();  // the alternatives are read from memory: before the gradient in place
+      T* dz = (T*)a.dz + row * a.ldd;
+      const RowGrad g(a, row, id, m, r.logZ, r.H);
+      h.repack();
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = tid + i * NT;
+        float f[Vec<T>::N];
+        g.template step<T>(h.d[i], s.first(v), f);
+        if (v < s.steps) s.store(dz, v, f);
+      }
+      if (tid < s.singles) dz[s.single(tid)] = (T)g.one(h.x, s.single(tid));
+    }
+    __syncthreads();  // the next row's shared values
+  }
+}
+
+// joins the segments of each row: one workgroup a row
+__global__ __launch_bounds__(256) void k_logprobs_join(const TokenArgs a, const RowSplit sp) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    const float* part = sp.part + row * sp.nseg * sp.stride;
+    float m = -INFINITY;  // every wave for itself
+    for (int q = lane; q < sp.nseg; q += 64) m = fmaxf(m, part[q * sp.stride]);
+    m = wave_max(m);
+    const float ref = m == -INFINITY ? 0.f : m;
+    double Z = 0, S = 0;
+    for (int q = lane; q < sp.nseg; q += 64) {
+      const float* p = part + q * sp.stride;
+      if (p[0] == -INFINITY && p[1] == 0.f) continue;
+      // S of the segment is about its own maximum mq: sum e (z - m) = f (S + Z (mq - m)), f = exp(s (mq - m))
+      const float dm = (p[0] == -INFINITY ? 0.f : p[0]) - ref, f = exp2f(dm * a.s * kLog2e);
+      Z += (double)f * p[1];
+      S += (double)f * (p[2] + (double)p[1] * fmaxf(dm, kLow));
+    }
+    Z = wave_sum(Z);
+    S = wave_sum(S);
+    const RowStat r(m, (float)Z, (float)S, a.s);
+    if (tid == 0) {
+      const int id = token_of(a, row);
+      const float z_id = id < 0 ? 0.f
+                                : a.dt == BF16 ? (float)((const __bf16*)a.z + row * a.ld)[id] : ((const float*)a.z + row * a.ld)[id];
+      write_row(a, row, r, z_id, id);
+    }
+    // the segments' lists are in order: the rank of a key is its place in its own list plus, in each other list, the
+    // number of larger keys
+    for (int e = tid; e < sp.nseg * a.K; e += 256) {
+      const int q = e / a.K;
+      const auto list = [&](int o) { return reinterpret_cast<const uint64_t*>(part + o * sp.stride + 4); };
+      const uint64_t key = list(q)[e - q * a.K];
+      if (key == 0) continue;  // the rest of a short last segment
+      int rank = e - q * a.K;
+      for (int o = 0; o < sp.nseg && rank < a.K; ++o) {
+        if (o == q) continue;
+        const uint64_t* l = list(o);
+        int lo = 0, hi = a.K;  // l[lo - 1] > key >= l[hi]
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (l[mid] > key) lo = mid + 1; else hi = mid;
+        }
+        rank += lo;
+      }
+      if (rank >= a.K) continue;
+      a.top_ids[row * a.K + rank] = (int)~(uint32_t)key;
+      a.top_logp[row * a.K + rank] = r.logp(unordered((uint32_t)(key >> 32)), a.s);
+    }
+  }
+}
+
+// ---- distillation ---------------------------------------------------------------------------------------------------
+// The listed tokens of a row are few: they are taken out of the row (their logits become -inf in the registers) and kept
+// in this list, so that the sum over the unlisted tokens, with its own maximum mt, needs no subtraction however little
+// they hold, and the passes over the row need no tests.
+struct List {
+  float q[POET_MAX_TOP], lq[POET_MAX_TOP], z[POET_MAX_TOP];  // teacher's probability and its logarithm; student's logit
+  int id[POET_MAX_TOP];   // -1: absent
+  float all[POET_MAX_TOP];  // for an id's first entry: the sum of q over its entries; else unused
+  float qt;               // TAIL: what the list leaves
+  int some, repeated;     // any entry; any id twice
+  float m, logZ, mt, logZt;  // the row's statistics
+  float C, scale;         // gradient: factors of the unlisted tokens, of the listed ones (grad_factors)
+};
+
+// One wave (all 64 lanes; entry k belongs to lane k % 64) loads row `row`'s list: the ids, the student's logits and, in
+// lq, the teacher's as they are. `z` is the student's row.
+template <class T> __device__ void load_list(List& L, const TokenArgs& a, int64_t row, const T* z) {
+  const int lane = threadIdx.x & 63;
+  for (int k = lane; k < a.K; k += 64) {
+    int id = a.t_ids[row * a.K + k];
     if (id < 0 || id >= a.V) id = -1;
     L.id[k] = id;
-    L.z[k] = id < 0 ? 0.f : ld(z, id);
-    L.lq[k] = id < 0 ? -INFINITY : a.t_z[(int64_t)row * a.K + k];
+    L.z[k] = id < 0 ? -INFINITY : (float)z[id];
+    L.lq[k] = id < 0 ? -INFINITY : a.t_z[row * a.K + k];
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int some = 0;
-    float tm = -INFINITY;
-    for (int k = 0; k < a.K; ++k) { some |= L.id[k] >= 0; tm = fmaxf(tm, L.lq[k]); }
-    double Q = 0;
-    if (a.tail) {
-      for (int k = 0; k < a.K; ++k) {
-        const double l = (double)L.lq[k] * a.ts - (a.t_lse ? a.t_lse[row] : 0.f);
-        L.lq[k] = (float)l; L.q[k] = (float)exp(l);
-        Q += exp(l);
-      }
-      L.qt = some ? fmaxf((float)(1.0 - Q), 0.f) : 0.f;
-    } else {
-      for (int k = 0; k < a.K; ++k) Q += exp(((double)L.lq[k] - tm) * a.ts);
-      for (int k = 0; k < a.K; ++k) {
-        const double l = ((double)L.lq[k] - tm) * a.ts - log(Q);
-        L.lq[k] = (float)l; L.q[k] = (float)exp(l);
-      }
-      L.qt = 0.f;
+  if (lane == 0) L.repeated = 0;
+}
+
+// The teacher's probabilities from a loaded list, by the same wave. The list's few logarithms are taken in 64 bits: the
+// loss is the small difference of the teacher's and the student's.
+__device__ void teach(List& L, const TokenArgs& a, int64_t row) {
+  const int lane = threadIdx.x & 63;
+  bool some = false, odd = false;
+  float tm = -INFINITY;
+  for (int k = lane; k < a.K; k += 64) {
+    some |= L.id[k] >= 0;
+    odd |= L.lq[k] != L.lq[k];
+    tm = fmaxf(tm, L.lq[k]);
+  }
+  some = __any(some);
+  tm = wave_max(tm);
+  if (!a.tail) some = some && (tm > -INFINITY || __any(odd));  // entries at -inf are as good as absent
+  const double off = a.tail ? (a.t_lse ? (double)a.t_lse[row] : 0.0) : (double)tm * a.ts;
+  double Q = 0;
+  for (int k = lane; k < a.K; k += 64)
+    if (some && L.id[k] >= 0) Q += exp((double)L.lq[k] * a.ts - off);
+  Q = wave_sum(Q);
+  const double lQ = a.tail || !some ? off : off + log(Q);
+  for (int k = lane; k < a.K; k += 64) {
+    const double l = (double)L.lq[k] * a.ts - lQ;
+    L.lq[k] = (float)l;
+    L.q[k] = L.all[k] = some && L.id[k] >= 0 ? (float)exp(l) : 0.f;
+  }
+  if (lane == 0) { L.some = some; L.qt = a.tail && some ? fmaxf((float)(1.0 - Q), 0.f) : 0.f; }
+}
+
+// Marks the repeated ids of a list (one wave, after teach and a barrier or wave_fence): `all` of an id's first entry is the sum of
+// its entries in their order, of the others -1.
+__device__ void join_repeated(List& L, int K) {
+  const int lane = threadIdx.x & 63;
+  float sum[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int k = lane + 64 * u;
+    sum[u] = 0.f;
+    if (k >= K || L.id[k] < 0) continue;
+    for (int o = 0; o < K; ++o) {
+      if (L.id[o] != L.id[k]) continue;
+      if (o < k) { sum[u] = -1.f; break; }
+      sum[u] += L.q[o];
     }
-    for (int k = 0; k < a.K; ++k)
-      if (L.id[k] < 0) L.q[k] = 0.f;
-    L.some = some;
   }
-  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (lane + 64 * u < K) L.all[lane + 64 * u] = sum[u];
 }
 
-__device__ __forceinline__ bool listed(const List& L, int K, int j) {
-  for (int k = 0; k < K; ++k)
-    if (L.id[k] == j) return true;
-  return false;
-}
+// An entry that stands for its token in sums over distinct tokens and in the gradient
+__device__ __forceinline__ bool stands(const List& L, int k) { return L.id[k] >= 0 && L.all[k] >= 0.f; }
 
-template <class T>
-__global__ __launch_bounds__(kThreads) void k_distill(const TokenArgs a) {
-  __shared__ double rd[kThreads / 64];
-  __shared__ float rf[kThreads / 64];
-  __shared__ List L;
-  const int row = blockIdx.x;
-  const T* z = (const T*)a.z + row * a.ld;
-  load_list(L, a, row, z);
-  const auto fmx = [](float x, float y) { return fmaxf(x, y); };
-  const auto add = [](double x, double y) { return x + y; };
-  float m = -INFINITY, mt = -INFINITY;  // of the whole row, of its unlisted part
-  for (int j = threadIdx.x; j < a.V; j += kThreads) {
-    const float v = ld(z, j);
-    m = fmaxf(m, v);
-    if (a.tail && !listed(L, a.K, j)) mt = fmaxf(mt, v);
-  }
-  m = block_all(wave_max(m), rf, fmx);
-  mt = block_all(wave_max(mt), rf, fmx);
-  const float ref = m == -INFINITY ? 0.f : m, reft = mt == -INFINITY ? 0.f : mt;
-  double Z = 0, Zt = 0;
-  for (int j = threadIdx.x; j < a.V; j += kThreads) {
-    const float v = ld(z, j);
-    Z += expf((v - ref) * a.s);
-    if (a.tail && !listed(L, a.K, j)) Zt += expf((v - reft) * a.s);
-  }
-  Z = block_all(wave_sum(Z), rd, add);
-  Zt = block_all(wave_sum(Zt), rd, add);
-  if (threadIdx.x) return;
-  const double logZ = log(Z), logZt = log(Zt);
+// The row's loss and statistics from its list and the unlisted tokens' maximum mt and sum Zt (about mt), by one wave:
+// {m, log Z} of the whole row and {mt, log Zt}.
+__device__ void finish_distill(List& L, const TokenArgs& a, int64_t row, float mt, double Zt) {
+  const int lane = threadIdx.x & 63;
+  float m = mt;
+  for (int k = lane; k < a.K; k += 64)
+    if (L.id[k] >= 0) m = fmaxf(m, L.z[k]);
+  m = wave_max(m);
+  const float ref = m == -INFINITY ? 0.f : m;
+  const double s = a.s;
+  double Z = 0;
+  for (int k = lane; k < a.K; k += 64)
+    if (stands(L, k)) Z += exp(((double)L.z[k] - ref) * s);
+  Z = wave_sum(Z);
+  if (Zt != 0.0) Z += Zt * exp(((double)(mt == -INFINITY ? 0.f : mt) - ref) * s);
   const bool none = m == -INFINITY && Z == 0.0;
+  const double logZ = log(Z), logZt = log(Zt);
   double loss = 0;
-  for (int k = 0; k < a.K; ++k)
-    if (L.q[k] > 0.f) loss += none ? INFINITY : (double)L.q[k] * (L.lq[k] - (((double)L.z[k] - ref) * a.s - logZ));
-  if (L.qt > 0.f) loss += none ? INFINITY : L.qt * (log((double)L.qt) - (logZt + ((double)reft - ref) * a.s - logZ));
-  a.loss[row] = L.some ? (float)loss : 0.f;
-  float* q = a.stats + (int64_t)row * 4;
-  q[0] = m; q[1] = (float)logZ; q[2] = a.tail ? mt : 0.f; q[3] = a.tail ? (float)logZt : 0.f;
-}
-
-template <class T>
-__global__ __launch_bounds__(kThreads) void k_distill_bwd(const TokenArgs a) {
-  __shared__ List L;
-  const int row = blockIdx.x;
-  const T* z = (const T*)a.z + row * a.ld;
-  T* dz = (T*)a.dz + row * a.ldd;
-  load_list(L, a, row, z);
-  const float* q = a.stats + (int64_t)row * 4;
-  const float m = q[0], logZ = q[1], mt = q[2], logZt = q[3];
-  const float w = L.some ? a.dloss[row] : 0.f;
-  const bool zero = w == 0.f || (m == -INFINITY && logZ == -INFINITY);
-  const float ref = m == -INFINITY ? 0.f : m, reft = mt == -INFINITY ? 0.f : mt;
-  for (int j = threadIdx.x; j < a.V; j += kThreads) {
-    float g = 0.f;
-    if (!zero) {
-      const float v = ld(z, j);
-      g = expf((v - ref) * a.s - logZ);
-      bool in = false;
-      float take = 0.f;
-      for (int k = 0; k < a.K; ++k)
-        if (L.id[k] == j) { in = true; take += L.q[k]; }
-      if (!in && a.tail && L.qt > 0.f && logZt > -INFINITY) take = L.qt * expf((v - reft) * a.s - logZt);
-      g = (g - take) * w * a.s;
-    }
-    st(dz, j, g);
+  for (int k = lane; k < a.K; k += 64)
+    if (L.q[k] > 0.f || L.q[k] != L.q[k]) loss += none ? INFINITY : (double)L.q[k] * (L.lq[k] - (((double)L.z[k] - ref) * s - logZ));
+  loss = wave_sum(loss);
+  if (L.qt > 0.f)
+    loss += none ? INFINITY : L.qt * (log((double)L.qt) - (logZt + ((double)(mt == -INFINITY ? 0.f : mt) - ref) * s - logZ));
+  if (lane == 0) {
+    a.loss[row] = L.some ? (float)loss : 0.f;
+    float* q = a.stats + row * 4;
+    q[0] = L.m = m; q[1] = L.logZ = (float)logZ; q[2] = L.mt = mt; q[3] = L.logZt = (float)logZt;
   }
 }
 
+// The gradient's factors from the row's statistics in L (one thread): unlisted tokens get C exp(s (z - mt)), listed ones
+// scale (exp(s (z - m) - log Z) - sum q).
+__device__ void grad_factors(List& L, const TokenArgs& a, int64_t row) {
+  const float w = L.some ? a.dloss[row] : 0.f;
+  const bool zero = w == 0.f || (L.m == -INFINITY && L.logZ == -INFINITY);
+  const float ref = L.m == -INFINITY ? 0.f : L.m;
+  float C = 0.f;
+  if (!zero && L.logZt != -INFINITY) {
+    C = expf(((L.mt == -INFINITY ? 0.f : L.mt) - ref) * a.s - L.logZ);
+    if (L.qt > 0.f) C -= L.qt * expf(-L.logZt);
+  }
+  L.scale = zero ? 0.f : w * a.s;
+  L.C = C * L.scale;
+}
+__device__ __forceinline__ float grad_listed(const List& L, int k, float s) {
+  const float ref = L.m == -INFINITY ? 0.f : L.m;
+  return L.scale == 0.f ? 0.f : L.scale * (expf((L.z[k] - ref) * s - L.logZ) - L.all[k]);
+}
+
+// One workgroup a row or segment, as k_logprobs; partials: mt, Zt.
+template <class T, int NT, int VPT>
+__global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowSplit sp) {
+  __shared__ List L;
+  __shared__ float sm[NT / 64], sz[NT / 64];
+  __shared__ uint32_t bits[NT * VPT / 4 + 1];  // the listed elements: a byte a step, then the single elements
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  for (int64_t w = blockIdx.x; w < (int64_t)a.T * sp.nseg; w += gridDim.x) {
+    const int64_t row = sp.nseg == 1 ? w : w / sp.nseg;
+    const int seg = sp.nseg == 1 ? 0 : (int)(w - row * sp.nseg);
+    const int base = seg * sp.len;
+    const T* z = (const T*)a.z + row * a.ld;
+    const int n = min(sp.len, a.V - base);
+    const Steps<T> s(z + base, n);
+    Held<T, NT, VPT> h;
+    h.load(s);
+    for (int i = tid; i <= NT * VPT / 4; i += NT) bits[i] = 0;
+    if (wave == 0) load_list<T>(L, a, row, z);
+    __syncthreads();
+    if (wave == 0) {
+      bool twice = false;
+      for (int k = lane; k < a.K; k += 64) {
+        const int j = L.id[k] - base;
+        if (L.id[k] < 0 || j < 0 || j >= n) continue;
+        const int at = j - s.head, v = at / Vec<T>::N;
+        const bool step = at >= 0 && v < s.steps;
+        const uint32_t b = 1u << (step ? v % 4 * 8 + at % Vec<T>::N : at < 0 ? j : j - s.steps * Vec<T>::N);
+        twice |= (atomicOr(&bits[step ? v / 4 : NT * VPT / 4], b) & b) != 0;
+      }
+      if (__any(twice) && lane == 0) L.repeated = 1;
+    }
+    __syncthreads();
+    if (tid < 32 && bits[NT * VPT / 4] >> tid & 1) h.x = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const uint32_t b = reinterpret_cast<const uint8_t*>(bits)[tid + i * NT];
+      if (b) {
+#pragma unroll
+        for (int k = 0; k < Vec<T>::N; ++k)
+          if (b >> k & 1) Vec<T>::none(h.d[i], k);
+      }
+    }
+    float mt = wave_max(h.max());
+    if (lane == 0) sm[wave] = mt;
+    __syncthreads();
+    mt = sm[0];
+#pragma unroll
+    for (int q = 1; q < NT / 64; ++q) mt = fmaxf(mt, sm[q]);
+    const float ref = mt == -INFINITY ? 0.f : mt, c = a.s * kLog2e;
+    float Z = 0.f;
+    h.repack();
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float zi = 0.f;
+#pragma unroll
+      for (int k = 0; k < Vec<T>::N; ++k) zi += exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
+      Z += zi;
+    }
+    Z = wave_sum(Z + exp2_fast((h.x - ref) * c));
+    if (lane == 0) sz[wave] = Z;
+    __syncthreads();
+    if (sp.nseg > 1) {
+      if (tid == 0) {
+        double Zt = 0;
+        for (int q = 0; q < NT / 64; ++q) Zt += sz[q];
+        float* p = sp.part + w * sp.stride;
+        p[0] = mt;
+        p[1] = (float)Zt;
+      }
+      __syncthreads();
+      continue;
+    }
+    if (wave == 0) {
+      double Zt = 0;
+      for (int q = 0; q < NT / 64; ++q) Zt += sz[q];
+      teach(L, a, row);
+      wave_fence();
+      if (L.repeated) join_repeated(L, a.K);
+      wave_fence();
+      finish_distill(L, a, row, mt, Zt);
+      if (a.dz && lane == 0) grad_factors(L, a, row);
+    }
+    __syncthreads();
+    if (a.dz) {
+      T* dz = (T*)a.dz + row * a.ldd;
+      const float C = L.C;
+      const bool zero = L.scale == 0.f;
+      h.repack();
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = tid + i * NT;
+        float f[Vec<T>::N];
+#pragma unroll
+        for (int k = 0; k < Vec<T>::N; ++k) f[k] = zero ? 0.f : C * exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
+        if (v < s.steps) s.store(dz, v, f);
+      }
+      if (tid < s.singles) dz[s.single(tid)] = (T)(zero ? 0.f : C * exp2_fast((h.x - ref) * c));
+      __syncthreads();  // the listed tokens' own, over what the steps wrote there
+      if (wave == 0)
+        for (int k = lane; k < a.K; k += 64)
+          if (stands(L, k)) dz[L.id[k]] = (T)grad_listed(L, k, a.s);
+    }
+    __syncthreads();
+  }
+}
+
+template <class T> __global__ __launch_bounds__(64) void k_distill_join(const TokenArgs a, const RowSplit sp) {
+  __shared__ List L;
+  const int lane = threadIdx.x;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    load_list<T>(L, a, row, (const T*)a.z + row * a.ld);
+    __syncthreads();
+    teach(L, a, row);
+    __syncthreads();
+    join_repeated(L, a.K);
+    __syncthreads();
+    const float* part = sp.part + row * sp.nseg * sp.stride;
+    float mt = -INFINITY;
+    for (int q = lane; q < sp.nseg; q += 64) mt = fmaxf(mt, part[q * sp.stride]);
+    mt = wave_max(mt);
+    double Zt = 0;
+    for (int q = lane; q < sp.nseg; q += 64) {
+      const float* p = part + q * sp.stride;
+      if (p[0] == -INFINITY && p[1] == 0.f) continue;
+      Zt += (double)p[1] * exp2f((p[0] == -INFINITY ? 0.f : p[0] - (mt == -INFINITY ? 0.f : mt)) * a.s * kLog2e);
+    }
+    finish_distill(L, a, row, mt, wave_sum(Zt));
+    __syncthreads();
+  }
+}
+
+// ---- the gradients after the forward -----------------------------------------------------------------------------
+constexpr int kGradThreads = 256, kGradSteps = 4;  // 16 KB of a row a workgroup
+
+// step v of the results at `out`, which need not be aligned like the logits
+template <class T> __device__ __forceinline__ void put_step(const Steps<T>& s, T* out, bool wide, int v, const float* f) {
+  if (wide) {
+    s.store(out, v, f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < Vec<T>::N; ++k) out[s.first(v) + k] = (T)f[k];
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(kGradThreads) void k_logprobs_bwd(const TokenArgs a, int chunks, int len) {
+  for (int64_t w = blockIdx.x; w < (int64_t)a.T * chunks; w += gridDim.x) {
+    const int64_t row = w / chunks;
+    const int base = (int)(w - row * chunks) * len;
+    const T* z = (const T*)a.z + row * a.ld;
+    T* dz = (T*)a.dz + row * a.ldd;
+    const int n = min(len, a.V - base);
+    const Steps<T> s(z + base, n);
+    Held<T, kGradThreads, kGradSteps> h;
+    const float* q = a.stats + row * 4;
+    RowGrad g(a, row, token_of(a, row), q[0], q[1], q[2]);
+    g.id = g.id < 0 ? INT32_MIN : g.id - base;  // in the chunk's own count
+    if (g.zero) {
+#pragma unroll
+      for (int i = 0; i < kGradSteps; ++i) h.d[i] = u32x4{0, 0, 0, 0};
+      h.x = 0.f;
+    } else {
+      h.load(s);
+    }
+    const bool wide = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+    dz += base;
+#pragma unroll
+    for (int i = 0; i < kGradSteps; ++i) {
+      const int v = threadIdx.x + i * kGradThreads;
+      float f[Vec<T>::N];
+      g.template step<T>(h.d[i], s.first(v), f);
+      if (v < s.steps) put_step(s, dz, wide, v, f);
+    }
+    if ((int)threadIdx.x < s.singles) dz[s.single(threadIdx.x)] = (T)g.one(h.x, s.single(threadIdx.x));
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a, int chunks, int len) {
+  __shared__ List L;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int64_t w = blockIdx.x; w < (int64_t)a.T * chunks; w += gridDim.x) {
+    const int64_t row = w / chunks;
+    const int base = (int)(w - row * chunks) * len;
+    const T* z = (const T*)a.z + row * a.ld;
+    T* dz = (T*)a.dz + row * a.ldd;
+    const int n = min(len, a.V - base);
+    const Steps<T> s(z + base, n);
+    Held<T, kGradThreads, kGradSteps> h;
+    h.load(s);
+    const float* q = a.stats + row * 4;
+    const float ref = q[2] == -INFINITY ? 0.f : q[2], c = a.s * kLog2e;
+    // the listed logits are read here, before this workgroup's steps may overwrite them in place; another workgroup
+    // may have overwritten those outside this chunk, which are not used
+    if (wave == 0) load_list<T>(L, a, row, z);
+    __syncthreads();
+    if (wave == 0) {
+      teach(L, a, row);
+      wave_fence();
+      join_repeated(L, a.K);
+      if (lane == 0) {
+        L.m = q[0]; L.logZ = q[1]; L.mt = q[2]; L.logZt = q[3];
+        grad_factors(L, a, row);
+      }
+    }
+    __syncthreads();
+    const bool wide = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+    const float C = L.C;
+    const bool zero = L.scale == 0.f;
+    dz += base;
+#pragma unroll
+    for (int i = 0; i < kGradSteps; ++i) {
+      const int v = threadIdx.x + i * kGradThreads;
+      float f[Vec<T>::N];
+#pragma unroll
+      for (int k = 0; k < Vec<T>::N; ++k) f[k] = zero ? 0.f : C * exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
+      if (v < s.steps) put_step(s, dz, wide, v, f);
+    }
+    if ((int)threadIdx.x < s.singles) dz[s.single(threadIdx.x)] = (T)(zero ? 0.f : C * exp2_fast((h.x - ref) * c));
+    __syncthreads();
+    if (wave == 0)
+      for (int k = lane; k < a.K; k += 64)
+        if (stands(L, k) && L.id[k] >= base && L.id[k] < base + n) dz[L.id[k] - base] = (T)grad_listed(L, k, a.s);
+    __syncthreads();
+  }
+}
+
+// ---- launches ----------------------------------------------------------------------------------------------------
+constexpr int kHeld = 1024 * 16;  // steps that the largest workgroup holds
+
+// How rows of V elements are split (a row of at most N-1 elements more than a workgroup's steps goes with those as its
+// single elements, however it is aligned)
+RowSplit split_of(int V, int dt, int K) {
+  const int n = dt == BF16 ? 8 : 4, cap = kHeld * n;
+  RowSplit sp;
+  if (V / n > kHeld) sp.nseg = (V + cap - 1) / cap;
+  sp.len = sp.nseg == 1 ? V : ((V + sp.nseg - 1) / sp.nseg + 63) / 64 * 64;  // <= cap, and whole steps
+  sp.stride = 4 + 2 * K;
+  sp.steps = sp.len / n;
+  return sp;
+}
+// a row's gradient can be written as its logits are read: 16 bytes at a time, every row
+bool same_alignment(const TokenArgs& a) {
+  const int64_t e = (int64_t)dtype_size(a.dt);
+  return ((reinterpret_cast<uintptr_t>(a.z) ^ reinterpret_cast<uintptr_t>(a.dz)) & 15) == 0 &&
+         (a.T == 1 || (a.ld - a.ldd) * e % 16 == 0);
+}
+dim3 grid_of(int64_t n) { return dim3((unsigned)std::min<int64_t>(n, kMaxBlocks)); }
+
+// f(type, threads, steps a thread) for the smallest workgroup that holds `steps`
+template <int A, int B> struct Size { static constexpr int NT = A, VPT = B; };
+template <class T, class F> void by_size(int steps, int64_t groups, F f) {
+  const bool few = groups < 512;
+  if (steps <= 512) f(T(), Size<256, 2>());
+  else if (steps <= 1024) f(T(), Size<256, 4>());
+  else if (!few && steps <= 2048) f(T(), Size<256, 8>());
+  else if (!few && steps <= 4096) f(T(), Size<256, 16>());
+  else if (steps <= 4096) f(T(), Size<1024, 4>());
+  else if (steps <= 8192) f(T(), Size<1024, 8>());
+  else f(T(), Size<1024, 16>());
+}
 template <class F> hipError_t by_type(int dt, F f) {
   if (dt == BF16) f(__bf16()); else f(float());
   return hipGetLastError();
@@ -249,21 +872,81 @@ template <class F> hipError_t by_type(int dt, F f) {
 
 }  // namespace
 
-hipError_t launch_logprobs(const TokenArgs& a, hipStream_t st) {
-  ProfScope prof(POET_K_HEAD, st, 6.0 * a.T * a.V, (double)a.T * a.V * dtype_size(a.dt));
-  return by_type(a.dt, [&](auto t) { hipLaunchKernelGGL(k_logprobs<decltype(t)>, dim3(a.T), dim3(kThreads), 0, st, a); });
+size_t logprobs_part_bytes(int T, int V, int dt, int K) {
+  const RowSplit sp = split_of(V, dt, K);
+  return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
+
+hipError_t launch_logprobs(const TokenArgs& args, float* part, hipStream_t st) {
+  TokenArgs a = args;
+  RowSplit sp = split_of(a.V, a.dt, a.K);
+  sp.part = part;
+  const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in a launch of its own
+  if (after) a.dz = nullptr;
+  {
+    const double e = dtype_size(a.dt), n = (double)a.T * a.V;
+    ProfScope prof(POET_K_HEAD, st, n * (a.dz ? 9 : 6), n * e * (a.dz ? 2 : 1));
+    const int64_t groups = (int64_t)a.T * sp.nseg;
+    by_type(a.dt, [&](auto t) {
+      by_size<decltype(t)>(sp.steps, groups, [&](auto u, auto z) {
+        using Z = decltype(z);
+        hipLaunchKernelGGL((k_logprobs<decltype(u), Z::NT, Z::VPT>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
+      });
+    });
+  }
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && sp.nseg > 1) {
+    ProfScope prof(POET_K_HEAD, st, 0, (double)a.T * sp.nseg * sp.stride * 4);
+    hipLaunchKernelGGL(k_logprobs_join, grid_of(a.T), dim3(256), 0, st, a, sp);
+    e = hipGetLastError();
+  }
+  return e != hipSuccess || !after ? e : launch_logprobs_bwd(args, st);
+}
+
 hipError_t launch_logprobs_bwd(const TokenArgs& a, hipStream_t st) {
+  const int n = a.dt == BF16 ? 8 : 4, len = kGradThreads * kGradSteps * n, chunks = (a.V + len - 1) / len;
   ProfScope prof(POET_K_HEAD, st, 6.0 * a.T * a.V, 2.0 * a.T * a.V * dtype_size(a.dt));
-  return by_type(a.dt, [&](auto t) { hipLaunchKernelGGL(k_logprobs_bwd<decltype(t)>, dim3(a.T), dim3(kThreads), 0, st, a); });
+  return by_type(a.dt, [&](auto t) {
+    hipLaunchKernelGGL(k_logprobs_bwd<decltype(t)>, grid_of((int64_t)a.T * chunks), dim3(kGradThreads), 0, st, a, chunks, len);
+  });
 }
-hipError_t launch_distill(const TokenArgs& a, hipStream_t st) {
-  ProfScope prof(POET_K_HEAD, st, 6.0 * a.T * a.V, (double)a.T * a.V * dtype_size(a.dt));
-  return by_type(a.dt, [&](auto t) { hipLaunchKernelGGL(k_distill<decltype(t)>, dim3(a.T), dim3(kThreads), 0, st, a); });
+
+size_t distill_part_bytes(int T, int V, int dt) {
+  const RowSplit sp = split_of(V, dt, 0);
+  return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
+
+hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
+  TokenArgs a = args;
+  RowSplit sp = split_of(a.V, a.dt, 0);
+  sp.part = part;
+  const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in a launch of its own
+  if (after) a.dz = nullptr;
+  {
+    const double e = dtype_size(a.dt), n = (double)a.T * a.V;
+    ProfScope prof(POET_K_HEAD, st, n * (a.dz ? 7 : 4), n * e * (a.dz ? 2 : 1));
+    const int64_t groups = (int64_t)a.T * sp.nseg;
+    by_type(a.dt, [&](auto t) {
+      by_size<decltype(t)>(sp.steps, groups, [&](auto u, auto z) {
+        using Z = decltype(z);
+        hipLaunchKernelGGL((k_distill<decltype(u), Z::NT, Z::VPT>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
+      });
+    });
+  }
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && sp.nseg > 1) {
+    ProfScope prof(POET_K_HEAD, st, 0, (double)a.T * sp.nseg * sp.stride * 4);
+    e = by_type(a.dt, [&](auto t) { hipLaunchKernelGGL(k_distill_join<decltype(t)>, grid_of(a.T), dim3(64), 0, st, a, sp); });
+  }
+  return e != hipSuccess || !after ? e : launch_distill_bwd(args, st);
+}
+
 hipError_t launch_distill_bwd(const TokenArgs& a, hipStream_t st) {
-  ProfScope prof(POET_K_HEAD, st, 6.0 * a.T * a.V, 2.0 * a.T * a.V * dtype_size(a.dt));
-  return by_type(a.dt, [&](auto t) { hipLaunchKernelGGL(k_distill_bwd<decltype(t)>, dim3(a.T), dim3(kThreads), 0, st, a); });
+  const int n = a.dt == BF16 ? 8 : 4, len = kGradThreads * kGradSteps * n, chunks = (a.V + len - 1) / len;
+  ProfScope prof(POET_K_HEAD, st, 4.0 * a.T * a.V, 2.0 * a.T * a.V * dtype_size(a.dt));
+  return by_type(a.dt, [&](auto t) {
+    hipLaunchKernelGGL(k_distill_bwd<decltype(t)>, grid_of((int64_t)a.T * chunks), dim3(kGradThreads), 0, st, a, chunks, len);
+  });
 }
 
 }  // namespace poet
