@@ -4,6 +4,10 @@
 // and, with n = r_h h', u = dx w_pre, b = r_y y (gradients of h', x in; of h, y, G, w_post, w_pre out):
 //   t = dh' + r_h (u - n mean(u n)),  dh = a t,  dw_pre = sum dx n,
 //   v = t G w_post,  dy = r_y (v - b mean(v b)),  dw_post = sum t G b,  dG = sum over the row's tokens of t w_post b.
+// Both are bound by HBM: every tensor is read once and written once. A token is one workgroup's: d/8 threads hold 8
+// columns each (16 bytes of bf16) in registers between the two means, and keep their columns' weights for all tokens
+// that the workgroup takes, loading the next token's columns while they work on one. In the backward a workgroup takes a
+// run of consecutive tokens and sums its weights' gradients in registers; a second launch adds the workgroups' sums.
 #include <algorithm>
 
 #include "../../include/poet.h"
@@ -12,159 +16,437 @@
 namespace poet {
 namespace {
 
-constexpr int kThreads = 256;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// ---- 8 columns of a row --------------------------------------------------------------------------------------------
+// WIDE: adjacent columns 8 g .. 8 g + 7 of group g, in 16-byte accesses (every row of every tensor 16-byte aligned; the
+// last group of an odd d element by element). Else: columns g + k NT of thread g, element by element, for any alignment.
+// Columns past d read as 0.
+template <class T, bool WIDE> struct Cols {
+  static constexpr bool kPacked = WIDE && sizeof(T) == 2;
+  u32x4 v[kPacked ? 1 : 2];
+  __device__ __forceinline__ float get(int k) const {
+    if constexpr (kPacked) {
+      const uint32_t w = v[0][k >> 1];
+      return __uint_as_float(k & 1 ? w & 0xffff0000u : w << 16);
+    } else {
+      return __uint_as_float(v[k >> 2][k & 3]);
+    }
+  }
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float r = 0.f;
-  for (int i = 0; i < kThreads / 64; ++i) r += red[i];
-  __syncthreads();
-  return r;
-}
-
-template <class TR, class TA>
-__global__ __launch_bounds__(kThreads) void k_norm_fwd(const NormArgs a) {
-  __shared__ float red[kThreads / 64];
-  const int64_t t = blockIdx.x;
-  const TR* h = (const TR*)a.h + t * a.ldh;
-  TR* ho = a.h_out ? (TR*)a.h_out + t * a.ldh : nullptr;
-  const TA* y = a.y ? (const TA*)a.y + t * a.ldy : nullptr;
-  const TA* g = a.gate ? (const TA*)a.gate + t / a.gate_tokens * a.ldg : nullptr;
-  float ry = 1.f;
-  if (a.w_post) {
-    float s = 0.f;
-    for (int j = threadIdx.x; j < a.d; j += kThreads) { const float v = (float)y[j]; s += v * v; }
-    ry = 1.f / sqrtf(block_sum(s, red) / a.d + a.eps);
+    for (auto& x : v) x = u32x4{0, 0, 0, 0};
   }
-  float s = 0.f;
-  for (int j = threadIdx.x; j < a.d; j += kThreads) {
-    float v = (float)h[j];
-    if (y) {
-      float r = (float)y[j];
-      if (a.w_post) r = r * ry * a.w_post[j];
-      if (g) r *= (float)g[j];
-      const TR o = (TR)(v * a.res_scale + r);
-      ho[j] = o;
-      v = (float)o;
-    }
-    s += v * v;
-  }
-  const float rh = a.x ? 1.f / sqrtf(block_sum(s, red) / a.d + a.eps) : 0.f;
-  if (a.x) {
-    const TR* src = ho ? ho : h;
-    TA* x = (TA*)a.x + t * a.ldx;
-    for (int j = threadIdx.x; j < a.d; j += kThreads) x[j] = (TA)((float)src[j] * rh * a.w_pre[j]);
-  }
-  if (threadIdx.x == 0) { a.rstd[2 * t] = ry; a.rstd[2 * t + 1] = rh; }
-}
-
-// the gradient t of h' at column j of token t, from the row's mean c1 = mean(u n)
-template <class TR, class TA>
-__device__ __forceinline__ float grad_h(const NormArgs& a, int64_t t, int j, float rh, float c1) {
-  float g = a.dh_out ? (float)((const TR*)a.dh_out)[t * a.ldh + j] : 0.f;
-  if (a.dx) {
-    const float n = (float)((const TR*)a.h)[t * a.ldh + j] * rh;
-    const float u = (float)((const TA*)a.dx)[t * a.ldx + j] * a.w_pre[j];
-    g += rh * (u - n * c1);
-  }
-  return g;
-}
-
-template <class TR, class TA>
-__global__ __launch_bounds__(kThreads) void k_norm_bwd(const NormArgs a, float* c1s) {
-  __shared__ float red[kThreads / 64];
-  const int64_t t = blockIdx.x;
-  const float ry = a.rstd[2 * t], rh = a.rstd[2 * t + 1];
-  float s = 0.f;
-  if (a.dx)
-    for (int j = threadIdx.x; j < a.d; j += kThreads)
-      s += (float)((const TA*)a.dx)[t * a.ldx + j] * a.w_pre[j] * (float)((const TR*)a.h)[t * a.ldh + j] * rh;
-  const float c1 = block_sum(s, red) / a.d;
-  const TA* y = a.y ? (const TA*)a.y + t * a.ldy : nullptr;
-  const TA* g = a.gate ? (const TA*)a.gate + t / a.gate_tokens * a.ldg : nullptr;
-  s = 0.f;
-  for (int j = threadIdx.x; j < a.d; j += kThreads)
-    if (a.w_post)
-      s += grad_h<TR, TA>(a, t, j, rh, c1) * (g ? (float)g[j] : 1.f) * a.w_post[j] * (float)y[j] * ry;
-  const float c2 = block_sum(s, red) / a.d;
-  for (int j = threadIdx.x; j < a.d; j += kThreads) {
-    const float dt = grad_h<TR, TA>(a, t, j, rh, c1);
-    if (a.dy) {
-      float v = dt * (g ? (float)g[j] : 1.f);
-      if (a.w_post) v = ry * (v * a.w_post[j] - (float)y[j] * ry * c2);
-      ((TA*)a.dy)[t * a.ldy + j] = (TA)v;
+  __device__ __forceinline__ void load(const T* row, int g, int NT, int d) {
+    zero();
+    if constexpr (WIDE) {
+      const int c = 8 * g;
+      if (c + 8 <= d) {
+#pragma unroll
+        for (unsigned i = 0; i < sizeof(v) / 16; ++i) v[i] = reinterpret_cast<const u32x4*>(row + c)[i];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + k < d) {
+            if constexpr (kPacked) v[0][k >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[c + k]) << (k & 1) * 16;
+            else v[k >> 2][k & 3] = __float_as_uint((float)row[c + k]);
+          }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (g + k * NT < d) v[k >> 2][k & 3] = __float_as_uint((float)row[g + k * NT]);
     }
   }
-  if (threadIdx.x == 0) c1s[t] = c1;
+};
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {  // one rounding to nearest even each
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const f2 x = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, b2));
 }
 
-// one thread a column: the sums over the tokens
-template <class TR, class TA>
-__global__ __launch_bounds__(64) void k_norm_bwd_cols(const NormArgs a, const float* c1s) {
-  const int j = blockIdx.x * 64 + threadIdx.x;
-  if (j >= a.d) return;
-  double pre = 0, post = 0, dg = 0;
-  for (int64_t t = 0; t < a.T; ++t) {
-    const float ry = a.rstd[2 * t], rh = a.rstd[2 * t + 1];
-    if (a.dx) pre += (float)((const TA*)a.dx)[t * a.ldx + j] * (float)((const TR*)a.h)[t * a.ldh + j] * rh;
-    if (!a.gate && !a.w_post) continue;
-    const float dt = grad_h<TR, TA>(a, t, j, rh, c1s[t]);
-    const float b = (float)((const TA*)a.y)[t * a.ldy + j] * (a.w_post ? ry : 1.f);
-    const float g = a.gate ? (float)((const TA*)a.gate)[t / a.gate_tokens * a.ldg + j] : 1.f;
-    post += dt * g * b;
-    if (a.gate) {
-      dg += dt * b * (a.w_post ? a.w_post[j] : 1.f);
-      if (t + 1 == a.T || (t + 1) % a.gate_tokens == 0) {
-        ((TA*)a.dgate)[t / a.gate_tokens * a.ldg + j] = (TA)(float)dg;
-        dg = 0;
+template <class T, bool WIDE> __device__ __forceinline__ void store8(T* row, int g, int NT, int d, const float* f) {
+  if constexpr (WIDE) {
+    const int c = 8 * g;
+    if (c + 8 <= d) {
+      if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<u32x4*>(row + c) = u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+      } else {
+        reinterpret_cast<float4*>(row + c)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(row + c)[1] = make_float4(f[4], f[5], f[6], f[7]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < d) row[c + k] = (T)f[k];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (g + k * NT < d) row[g + k * NT] = (T)f[k];
+  }
+}
+
+template <class T> __device__ __forceinline__ float rounded(float x) { return (float)(T)x; }
+
+// ---- sums over a workgroup -----------------------------------------------------------------------------------------
+template <int CTRL, int ROWS> __device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {  // in every lane; every lane is active
+  v += dpp<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+  v += dpp<0x112, 0xf>(v);
+  v += dpp<0x114, 0xf>(v);
+  v += dpp<0x118, 0xf>(v);
+  v += dpp<0x142, 0xa>(v);  // row_bcast 15, 31
+  v += dpp<0x143, 0xc>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+// red: two sets of a float a wave, used in turn, so that one barrier a sum is enough
+__device__ __forceinline__ float block_sum(float v, float (*red)[16], int& turn) {
+  v = wave_sum(v);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
+  float* r = red[turn ^= 1];
+  if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int i = 0; i < waves; ++i) s += r[i];
+  return s;
+}
+
+// ---- forward --------------------------------------------------------------------------------------------------------
+template <class TR, class TA, int VPT, bool WIDE>
+__global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs a) {
+  __shared__ float red[2][16];
+  const int tid = threadIdx.x, NT = blockDim.x, d = a.d;
+  int turn = 0;
+  const float inv_d = 1.f / (float)d;
+  Cols<float, WIDE> wq[VPT], wp[VPT];
+  Cols<TR, WIDE> h[VPT];
+  Cols<TA, WIDE> y[VPT], g[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = WIDE ? tid + i * NT : tid + i * 8 * NT;
+    if (a.w_post) wq[i].load(a.w_post, c, NT, d);
+    if (a.w_pre) wp[i].load(a.w_pre, c, NT, d);
+  }
+  const auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = WIDE ? tid + i * NT : tid + i * 8 * NT;
+      h[i].load((const TR*)a.h + t * a.ldh, c, NT, d);
+      if (a.y) y[i].load((const TA*)a.y + t * a.ldy, c, NT, d);
+      if (a.gate) g[i].load((const TA*)a.gate + (a.gate_tokens == 1 ? t : t / a.gate_tokens) * a.ldg, c, NT, d);
+    }
+  };
+  if (VPT == 1) fetch(blockIdx.x);  // two groups a thread leave no registers for the next token's columns
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    if (VPT > 1) fetch(t);
+    float f[VPT][8], r[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        f[i][k] = h[i].get(k);
+        r[i][k] = a.y ? y[i].get(k) : 0.f;
+      }
+    float ry = 1.f, s = 0.f;
+    if (a.w_post) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = fmaf(r[i][k], r[i][k], s);
+      ry = 1.f / sqrtf(block_sum(s, red, turn) * inv_d + a.eps);
+    }
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (a.y) {
+          float b = r[i][k];
+          if (a.w_post) b = b * ry * wq[i].get(k);
+          if (a.gate) b *= g[i].get(k);
+          f[i][k] = rounded<TR>(fmaf(f[i][k], a.res_scale, b));  // the norm reads the residual stream as it is kept
+        }
+        s = fmaf(f[i][k], f[i][k], s);
+      }
+    if (VPT == 1 && t + gridDim.x < a.T) fetch(t + gridDim.x);
+    if (a.h_out) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        store8<TR, WIDE>((TR*)a.h_out + t * a.ldh, WIDE ? tid + i * NT : tid + i * 8 * NT, NT, d, f[i]);
+    }
+    float rh = 0.f;
+    if (a.x) {
+      rh = 1.f / sqrtf(block_sum(s, red, turn) * inv_d + a.eps);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[i][k] = f[i][k] * rh * wp[i].get(k);
+        store8<TA, WIDE>((TA*)a.x + t * a.ldx, WIDE ? tid + i * NT : tid + i * 8 * NT, NT, d, f[i]);
       }
     }
+    if (tid == 0) { a.rstd[2 * t] = ry; a.rstd[2 * t + 1] = rh; }
   }
-  if (a.dw_pre) a.dw_pre[j] = (float)pre;
-  if (a.dw_post) a.dw_post[j] = (float)post;
 }
 
-// last, so that dh may be dh_out
-template <class TR, class TA>
-__global__ __launch_bounds__(kThreads) void k_norm_bwd_dh(const NormArgs a, const float* c1s) {
-  const int64_t t = blockIdx.x;
-  for (int j = threadIdx.x; j < a.d; j += kThreads)
-    ((TR*)a.dh)[t * a.ldh + j] = (TR)(a.res_scale * grad_h<TR, TA>(a, t, j, a.rstd[2 * t + 1], c1s[t]));
-}
+// ---- backward -------------------------------------------------------------------------------------------------------
+// How the tokens go to workgroups: chunk p takes [t0, t1) below. Either a chunk holds whole runs of tokens that share a
+// gate row (split == 1: a row's gradient is summed and written by one workgroup), or a run is `split` chunks, whose sums
+// of the row's gradient the second launch adds.
+struct NormPlan {
+  int chunks = 0, len = 0, split = 1;
+  int run = 1;          // tokens a gate row; split > 1 only
+};
 
-template <class F> hipError_t by_types(int rdt, int adt, F f) {
-  if (rdt == BF16) {
-    if (adt == BF16) f(__bf16(), __bf16()); else f(__bf16(), float());
+__host__ __device__ inline void chunk_range(const NormPlan& p, int T, int c, int64_t& t0, int64_t& t1) {
+  if (p.split == 1) {
+    t0 = (int64_t)c * p.len;
+    t1 = t0 + p.len;
   } else {
-    if (adt == BF16) f(float(), __bf16()); else f(float(), float());
+    const int64_t r = c / p.split;
+    t0 = r * p.run + (int64_t)(c % p.split) * p.len;
+    t1 = t0 + p.len;
+    if (t1 > (r + 1) * p.run) t1 = (r + 1) * p.run;
+  }
+  if (t1 > T) t1 = T;
+}
+
+template <class TR, class TA, int VPT, bool WIDE>
+__global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs a, const NormPlan p, float* part) {
+  __shared__ float red[2][16];
+  const int tid = threadIdx.x, NT = blockDim.x, d = a.d;
+  int turn = 0;
+  const float inv_d = 1.f / (float)d;
+  int64_t t0, t1;
+  chunk_range(p, a.T, blockIdx.x, t0, t1);
+  Cols<float, WIDE> wq[VPT], wp[VPT];
+  Cols<TR, WIDE> h[VPT], e[VPT];
+  Cols<TA, WIDE> y[VPT], g[VPT], x[VPT];
+  float spre[VPT][8], spost[VPT][8], sg[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = WIDE ? tid + i * NT : tid + i * 8 * NT;
+    if (a.w_post) wq[i].load(a.w_post, c, NT, d);
+    if (a.w_pre) wp[i].load(a.w_pre, c, NT, d);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) spre[i][k] = spost[i][k] = sg[i][k] = 0.f;
+  }
+  float ry = 1.f, rh = 0.f;
+  const auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = WIDE ? tid + i * NT : tid + i * 8 * NT;
+      if (a.dx) { h[i].load((const TR*)a.h + t * a.ldh, c, NT, d); x[i].load((const TA*)a.dx + t * a.ldx, c, NT, d); }
+      if (a.dh_out) e[i].load((const TR*)a.dh_out + t * a.ldh, c, NT, d);
+      if (a.y) y[i].load((const TA*)a.y + t * a.ldy, c, NT, d);
+      if (a.gate) g[i].load((const TA*)a.gate + (a.gate_tokens == 1 ? t : t / a.gate_tokens) * a.ldg, c, NT, d);
+    }
+    ry = a.w_post ? a.rstd[2 * t] : 1.f;
+    rh = a.rstd[2 * t + 1];
+  };
+  if (VPT == 1 && t0 < t1) fetch(t0);
+  for (int64_t t = t0; t < t1; ++t) {
+    if (VPT > 1) fetch(t);
+    float f[VPT][8], b[VPT][8], v[VPT][8];
+    const float ryt = ry, rht = rh;
+    float s = 0.f;
+    if (a.dx) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float n = h[i].get(k) * rht, dx = x[i].get(k);
+          f[i][k] = dx * wp[i].get(k);
+          v[i][k] = n;
+          spre[i][k] = fmaf(dx, n, spre[i][k]);
+          s = fmaf(f[i][k], n, s);
+        }
+      const float c1 = block_sum(s, red, turn) * inv_d;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[i][k] = rht * fmaf(-v[i][k], c1, f[i][k]) + (a.dh_out ? e[i].get(k) : 0.f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[i][k] = e[i].get(k);
+    }
+    // f: the gradient of h'. Of the block's output: v before its norm's mean, b the normalized output.
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        b[i][k] = a.y ? y[i].get(k) * ryt : 0.f;
+        const float tg = a.gate ? f[i][k] * g[i].get(k) : f[i][k];
+        v[i][k] = a.w_post ? tg * wq[i].get(k) : tg;
+        spost[i][k] = fmaf(tg, b[i][k], spost[i][k]);
+        if (a.gate) sg[i][k] = fmaf(a.w_post ? f[i][k] * wq[i].get(k) : f[i][k], b[i][k], sg[i][k]);
+        s = fmaf(v[i][k], b[i][k], s);
+      }
+    if (VPT == 1 && t + 1 < t1) fetch(t + 1);
+    if (a.gate && p.split == 1 && (a.gate_tokens == 1 || t + 1 == t1 || (t + 1) % a.gate_tokens == 0)) {
+      const int64_t gr = a.gate_tokens == 1 ? t : t / a.gate_tokens;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        store8<TA, WIDE>((TA*)a.dgate + gr * a.ldg, WIDE ? tid + i * NT : tid + i * 8 * NT, NT, d, sg[i]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sg[i][k] = 0.f;
+      }
+    }
+    if (a.w_post) {
+      const float c2 = block_sum(s, red, turn) * inv_d;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = ryt * fmaf(-b[i][k], c2, v[i][k]);
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = WIDE ? tid + i * NT : tid + i * 8 * NT;
+      if (a.dy) store8<TA, WIDE>((TA*)a.dy + t * a.ldy, c, NT, d, v[i]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[i][k] *= a.res_scale;
+      store8<TR, WIDE>((TR*)a.dh + t * a.ldh, c, NT, d, f[i]);
+    }
+  }
+  // this chunk's sums: [chunk][pre, post, gate row][d]
+  float* q = part + (int64_t)blockIdx.x * 3 * d;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = WIDE ? 8 * (tid + i * NT) + k : tid + (i * 8 + k) * NT;
+      if (c >= d) continue;
+      if (a.dw_pre) q[c] = spre[i][k];
+      if (a.dw_post) q[d + c] = spost[i][k];
+      if (p.split > 1) q[2 * (int64_t)d + c] = sg[i][k];
+    }
+}
+
+// Adds the chunks' sums: y = 0, 1: all chunks into dw_pre, dw_post; y = 2 + r: the chunks of gate row r (stored as TA).
+// 64 columns a workgroup, 16 threads a column that take every 16th chunk, in a fixed order.
+template <class TA>
+__global__ __launch_bounds__(1024) void k_norm_sums(const NormArgs a, const NormPlan p, const float* part, int rows) {
+  __shared__ float red[16][64];
+  const int c = blockIdx.x * 64 + (threadIdx.x & 63), lane = threadIdx.x >> 6;
+  for (int64_t o = blockIdx.y; o < 2 + rows; o += gridDim.y) {
+    const bool skip = (o == 0 && !a.dw_pre) || (o == 1 && !a.dw_post);  // uniform
+    if (skip) continue;
+    const int64_t first = o < 2 ? 0 : (o - 2) * p.split, count = o < 2 ? p.chunks : p.split;
+    const float* q = part + (first * 3 + (o < 2 ? o : 2)) * a.d + c;
+    float s = 0.f;
+    if (c < a.d) {
+#pragma unroll 4
+      for (int64_t i = lane; i < count; i += 16) s += q[i * 3 * a.d];
+    }
+    red[lane][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (lane == 0 && c < a.d) {
+#pragma unroll
+      for (int i = 1; i < 16; ++i) s += red[i][threadIdx.x];
+      if (o == 0) a.dw_pre[c] = s;
+      else if (o == 1) a.dw_post[c] = s;
+      else ((TA*)a.dgate)[(o - 2) * a.ldg + c] = (TA)s;
+    }
+    __syncthreads();
+  }
+}
+
+// ---- launches -------------------------------------------------------------------------------------------------------
+int threads_of(int d) { return d <= 8192 ? (d + 511) / 512 * 64 : 1024; }
+
+NormPlan plan_of(int T, int d, int gate_tokens) {
+  // about 16 waves a CU (256 CUs) in one round of workgroups, but at most 256 tokens in a row of float32 additions
+  const int groups = std::max(1, 4096 / (threads_of(d) / 64));
+  const int len = std::min(256, std::max(1, (T + groups - 1) / groups));
+  NormPlan p;
+  p.len = len;
+  const int run = std::min(gate_tokens, T);
+  if (run > len) {
+    p.split = (run + len - 1) / len;
+    p.len = (run + p.split - 1) / p.split;
+    p.run = run;
+    p.chunks = (T + run - 1) / run * p.split;
+  } else {
+    if (run > 1) p.len = len / run * run;
+    p.chunks = (T + p.len - 1) / p.len;
+  }
+  return p;
+}
+
+bool al16(const void* p, int64_t ld, size_t e) { return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * (int64_t)e % 16 == 0); }
+
+bool wide_of(const NormArgs& a) {
+  const size_t r = dtype_size(a.res_dt), v = dtype_size(a.act_dt);
+  return al16(a.h, a.ldh, r) && al16(a.h_out, a.ldh, r) && al16(a.dh_out, a.ldh, r) && al16(a.dh, a.ldh, r) &&
+         al16(a.y, a.ldy, v) && al16(a.dy, a.ldy, v) && al16(a.gate, a.ldg, v) && al16(a.dgate, a.ldg, v) &&
+         al16(a.x, a.ldx, v) && al16(a.dx, a.ldx, v) && al16(a.w_post, 0, 4) && al16(a.w_pre, 0, 4);
+}
+
+template <int V, bool W> struct Form { static constexpr int VPT = V; static constexpr bool WIDE = W; };
+template <class F> hipError_t by_form(const NormArgs& a, F f) {
+  const auto types = [&](auto form) {
+    if (a.res_dt == BF16) {
+      if (a.act_dt == BF16) f(__bf16(), __bf16(), form); else f(__bf16(), float(), form);
+    } else {
+      if (a.act_dt == BF16) f(float(), __bf16(), form); else f(float(), float(), form);
+    }
+  };
+  if (a.d <= 8192) {
+    if (wide_of(a)) types(Form<1, true>()); else types(Form<1, false>());
+  } else {
+    if (wide_of(a)) types(Form<2, true>()); else types(Form<2, false>());
   }
   return hipGetLastError();
 }
 
+double moved(const NormArgs& a, int res, int act) {
+  const double n = (double)a.T * a.d;
+  const double rows = a.gate ? (double)((a.T + a.gate_tokens - 1) / a.gate_tokens) : 0;
+  return n * res * dtype_size(a.res_dt) + n * act * dtype_size(a.act_dt) + rows * a.d * dtype_size(a.act_dt);
+}
+
 }  // namespace
 
-size_t block_norm_bytes(int T, int d, int gate_tokens) { (void)d; (void)gate_tokens; return (size_t)T * 4 + 256; }
+size_t block_norm_bytes(int T, int d, int gate_tokens) { return (size_t)plan_of(T, d, gate_tokens).chunks * 3 * d * 4; }
 
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st) {
-  ProfScope prof(POET_K_NORM, st, 0, 0);
-  return by_types(a.res_dt, a.act_dt, [&](auto r, auto v) {
-    hipLaunchKernelGGL((k_norm_fwd<decltype(r), decltype(v)>), dim3(a.T), dim3(kThreads), 0, st, a);
+  ProfScope prof(POET_K_NORM, st, 10.0 * a.T * a.d, moved(a, a.y ? 2 : 1, (a.y ? 1 : 0) + (a.x ? 1 : 0)));
+  const int nt = threads_of(a.d);
+  const int grid = std::min(a.T, 256 * std::max(1, 2048 / nt));
+  return by_form(a, [&](auto r, auto v, auto form) {
+    using F = decltype(form);
+    hipLaunchKernelGGL((k_norm_fwd<decltype(r), decltype(v), F::VPT, F::WIDE>), dim3(grid), dim3(nt), 0, st, a);
   });
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, void* ws, hipStream_t st) {
-  float* c1s = reinterpret_cast<float*>(ws);
-  ProfScope prof(POET_K_NORM, st, 0, 0);
-  return by_types(a.res_dt, a.act_dt, [&](auto r, auto v) {
-    using TR = decltype(r);
-    using TA = decltype(v);
-    hipLaunchKernelGGL((k_norm_bwd<TR, TA>), dim3(a.T), dim3(kThreads), 0, st, a, c1s);
-    hipLaunchKernelGGL((k_norm_bwd_cols<TR, TA>), dim3((a.d + 63) / 64), dim3(64), 0, st, a, c1s);
-    hipLaunchKernelGGL((k_norm_bwd_dh<TR, TA>), dim3(a.T), dim3(kThreads), 0, st, a, c1s);
-  });
+  float* part = reinterpret_cast<float*>(ws);
+  const NormPlan p = plan_of(a.T, a.d, a.gate ? a.gate_tokens : 0);
+  {
+    ProfScope prof(POET_K_NORM, st, 25.0 * a.T * a.d,
+                   moved(a, 1 + (a.dx ? 1 : 0) + (a.dh_out ? 1 : 0), (a.dx ? 1 : 0) + (a.y ? 1 : 0) + (a.dy ? 1 : 0)));
+    const hipError_t e = by_form(a, [&](auto r, auto v, auto form) {
+      using F = decltype(form);
+      hipLaunchKernelGGL((k_norm_bwd<decltype(r), decltype(v), F::VPT, F::WIDE>), dim3(p.chunks), dim3(threads_of(a.d)), 0,
+                         st, a, p, part);
+    });
+    if (e != hipSuccess) return e;
+  }
+  const int rows = p.split > 1 ? (a.T + p.run - 1) / p.run : 0;
+  if (!a.dw_pre && !a.dw_post && rows == 0) return hipSuccess;
+  ProfScope prof(POET_K_NORM, st, 0, (double)p.chunks * 2 * a.d * 4);
+  const dim3 grid((a.d + 63) / 64, std::min(2 + rows, 65535));
+  if (a.act_dt == BF16) hipLaunchKernelGGL(k_norm_sums<__bf16>, grid, dim3(1024), 0, st, a, p, part, rows);
+  else hipLaunchKernelGGL(k_norm_sums<float>, grid, dim3(1024), 0, st, a, p, part, rows);
+  return hipGetLastError();
 }
 
 }  // namespace poet
