@@ -140,14 +140,23 @@ __device__ __forceinline__ uint64_t rank_key(float z, int j) {
   return (uint64_t)(z != z ? 0u : ordered(z)) << 32 | (uint32_t)~j;
 }
 
+// threadIdx.x, newly for each use: without it the compiler keeps the 64-bit places of all steps from one loop over them
+// to the next, in registers that it does not have
+__device__ __forceinline__ int lane_id() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 // ---- one row or segment in registers ---------------------------------------------------------------------------
 template <class T, int NT, int VPT> struct Held {
   u32x4 d[VPT];  // step threadIdx.x + i NT; -inf where there is none
   float x;       // single element threadIdx.x; -inf where there is none
   __device__ __forceinline__ void load(const Steps<T>& s) {
+    const int tid = lane_id();
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * NT;
+      const int v = tid + i * NT;
       d[i][0] = d[i][1] = d[i][2] = d[i][3] = Vec<T>::kNone;
       if (v < s.steps) d[i] = s.load(v);
     }
@@ -169,25 +178,28 @@ template <class T, int NT, int VPT> struct Held {
   }
 };
 
-template <int NT> struct Shared {
+constexpr int kSlots = 32;   // threads whose steps are looked through at a time
+template <int NT, int VPT> struct Shared {
   float m[NT / 64], z[NT / 64], s[NT / 64];
   float tmax[NT];           // each thread's largest logit
+  uint16_t slot[NT];        // its place among the threads that can hold one of the best; 0xffff: it cannot
+  u32x4 held[VPT][kSlots];  // steps of the threads of kSlots such places
+  int first[kSlots];        // and which threads they are
   uint64_t cand[kCand];
-  uint16_t win[NT];         // threads that can hold one of the best
   uint64_t best[NT / 64];
   float tau;
   int nwin, ncand;
 };
 
-// The K best alternatives of a row or segment, ranked, as out(rank, key).
+// The K best alternatives of a row or segment of n elements, ranked, as out(rank, key).
 // Threads' own maxima bound them: with tau the K-th largest of those, K elements are >= tau, and an element >= tau sits
-// with a thread whose maximum is >= tau. One wave finds tau bit by bit and lists those threads, a little over K of them;
-// the waves read the elements of one listed thread at a time again (from the cache: 64 lanes side by side, where a scan
-// of the registers would cost every wave all its steps), and the few >= tau are ranked against each other. Rows where
-// that is not few (many ties, fewer threads with logits than K), or that hold a NaN, are read again K times.
+// with a thread whose maximum is >= tau. One wave finds tau bit by bit and numbers those threads, a little over K of them;
+// they leave their steps in LDS, where all threads look through them (a scan of the registers would cost every wave all
+// its steps, reading the elements again a trip to memory a thread), and the few >= tau are ranked against each other.
+// Rows where that is not few (many ties, fewer threads with logits than K), or that hold a NaN, are read again K times.
 template <class T, int NT, int VPT, class Out>
-__device__ void best_of(const Steps<T>& s, int base, int n, int K, float tmax, bool sure,
-                        Shared<NT>& sh, Out out) {
+__device__ void best_of(const Held<T, NT, VPT>& h, const Steps<T>& s, int base, int n, int K, float tmax, bool sure,
+                        Shared<NT, VPT>& sh, Out out) {
   constexpr int N = Vec<T>::N;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (sure) {  // uniform
@@ -200,40 +212,50 @@ __device__ void best_of(const Steps<T>& s, int base, int n, int K, float tmax, b
       // bf16 logits differ in the upper 16 bits only; 10 bits less than float32's 32 let in a few threads more
       for (int bit = 31; bit >= (N == 8 ? 16 : 10); --bit) {
         const uint32_t c = t | 1u << bit;
-        int n = 0;
+        int m = 0;
 #pragma unroll
-        for (int q = 0; q < NT / 64; ++q) n += __popcll(__ballot(key[q] >= c));
-        if (n >= K) t = c;
-        if (n == K) break;
+        for (int q = 0; q < NT / 64; ++q) m += __popcll(__ballot(key[q] >= c));
+        if (m >= K) t = c;
+        if (m == K) break;
       }
-      int n = 0;
+      int m = 0;
 #pragma unroll
       for (int q = 0; q < NT / 64; ++q) {
         const uint64_t b = __ballot(key[q] >= t);
-        if (key[q] >= t) sh.win[n + __popcll(b & ((1ull << lane) - 1))] = (uint16_t)(q * 64 + lane);
-        n += __popcll(b);
+        sh.slot[q * 64 + lane] = key[q] >= t ? (uint16_t)(m + __popcll(b & ((1ull << lane) - 1))) : (uint16_t)0xffff;
+        m += __popcll(b);
       }
-      if (lane == 0) { sh.nwin = n; sh.ncand = 0; sh.tau = unordered(t); }
+      if (lane == 0) { sh.nwin = m; sh.ncand = 0; sh.tau = unordered(t); }
     }
     __syncthreads();
     const float tau = sh.tau;
-    const int nwin = sh.nwin;
+    const int nwin = sh.nwin, slot = sh.slot[tid];
     sure = tau > -INFINITY && nwin <= 2 * K + 64;
     if (sure) {
-      for (int w = wave; w < nwin; w += NT / 64) {
-        const int v0 = sh.win[w];
+      const auto take = [&](float z, int j) {
+        if (z >= tau) {
+          const int c = atomicAdd(&sh.ncand, 1);
+          if (c < kCand) sh.cand[c] = rank_key(z, base + j);
+        }
+      };
+      if (tid < s.singles) take(h.x, s.single(tid));
+      for (int w0 = 0; w0 < nwin; w0 += kSlots) {
+        if (w0 > 0) __syncthreads();
+        if (slot >= w0 && slot < w0 + kSlots) {
 #pragma unroll
-        for (int t0 = 0; t0 < VPT * N + 1; t0 += 64) {
-          const int t = t0 + lane, v = v0 + t / N * NT;  // element t of the thread's, the last one its single element
-          const bool step = t < VPT * N && v < s.steps, single = t == VPT * N && v0 < s.singles;
-          if (step || single) {
-            const int j = step ? s.first(v) + t % N : s.single(v0);
-            const float z = (float)s.p[j];
-            if (z >= tau) {
-              const int c = atomicAdd(&sh.ncand, 1);
-              if (c < kCand) sh.cand[c] = rank_key(z, base + j);
-            }
-          }
+          for (int i = 0; i < VPT; ++i) sh.held[i][slot - w0] = h.d[i];
+          sh.first[slot - w0] = tid;
+        }
+        __syncthreads();
+        const int ns = min(kSlots, nwin - w0);
+        for (int u = tid; u < VPT * kSlots; u += NT) {
+          const int w = u % kSlots, i = u / kSlots;
+          if (w >= ns) continue;
+          const int v = sh.first[w] + i * NT;
+          if (v >= s.steps) continue;
+          const u32x4 d = sh.held[i][w];
+#pragma unroll
+          for (int k = 0; k < N; ++k) take(Vec<T>::get(d, k), s.first(v) + k);
         }
       }
       __syncthreads();
@@ -339,7 +361,7 @@ struct RowGrad {
 // m, Z, S, -, then the K best keys).
 template <class T, int NT, int VPT>
 __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const RowSplit sp) {
-  __shared__ Shared<NT> sh;
+  __shared__ Shared<NT, VPT> sh;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   for (int64_t w = blockIdx.x; w < (int64_t)a.T * sp.nseg; w += gridDim.x) {
     const int64_t row = sp.nseg == 1 ? w : w / sp.nseg;
@@ -388,31 +410,32 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
 #pragma unroll
     for (int q = 1; q < NT / 64; ++q) { Z += sh.z[q]; S += sh.s[q]; }
     const RowStat r(m, Z, S, a.s);
-    if (sp.nseg > 1) {
-      float* p = sp.part + w * sp.stride;
-      if (tid == 0) { p[0] = m; p[1] = Z; p[2] = S; }
-      const int K = min(a.K, n);
-      if (K > 0)
-        best_of<T, NT, VPT>(s, base, n, K, tmax, Z == Z, sh,
-                            [&](int k, uint64_t key) { reinterpret_cast<uint64_t*>(p + 4)[k] = key; });
-      for (int k = K + tid; k < a.K; k += NT) reinterpret_cast<uint64_t*>(p + 4)[k] = 0;  // a short last segment
-      __syncthreads();
-      continue;
+    float* part = sp.nseg > 1 ? sp.part + w * sp.stride : nullptr;
+    if (tid == 0) {
+      if (part) { part[0] = m; part[1] = Z; part[2] = S; }
+      else write_row(a, row, r, z_id, id);
     }
-    if (tid == 0) write_row(a, row, r, z_id, id);
-    if (a.K > 0)
-      best_of<T, NT, VPT>(s, 0, n, a.K, tmax, Z == Z, sh, [&](int k, uint64_t key) {
-        a.top_ids[row * a.K + k] = (int)~(uint32_t)key;
-        a.top_logp[row * a.K + k] = r.logp(unordered((uint32_t)(key >> 32)), a.s);
+    if (a.K > 0) {
+      best_of<T, NT, VPT>(h, s, base, n, min(a.K, n), tmax, Z == Z, sh, [&](int k, uint64_t key) {
+        if (part) {
+          reinterpret_cast<uint64_t*>(part + 4)[k] = key;
+        } else {
+          a.top_ids[row * a.K + k] = (int)~(uint32_t)key;
+          a.top_logp[row * a.K + k] = r.logp(unordered((uint32_t)(key >> 32)), a.s);
+        }
       });
+      if (part)
+        for (int k = n + tid; k < a.K; k += NT) reinterpret_cast<uint64_t*>(part + 4)[k] = 0;  // a short last segment
+    }
     if (a.dz) {
-      if (a.K > 0) __syncthreads();  // the alternatives are read from memory: before the gradient in place
+      if (a.K > 0) __syncthreads();  // the alternatives may be read from memory: before the gradient in place
       T* dz = (T*)a.dz + row * a.ldd;
       const RowGrad g(a, row, id, m, r.logZ, r.H);
       h.repack();
+      const int t0 = lane_id();
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int v = tid + i * NT;
+        const int v = t0 + i * NT;
         float f[Vec<T>::N];
         g.template step<T>(h.d[i], s.first(v), f);
         if (v < s.steps) s.store(dz, v, f);
@@ -692,9 +715,10 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
       const float C = L.C;
       const bool zero = L.scale == 0.f;
       h.repack();
+      const int t0 = lane_id();
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int v = tid + i * NT;
+        const int v = t0 + i * NT;
         float f[Vec<T>::N];
 #pragma unroll
         for (int k = 0; k < Vec<T>::N; ++k) f[k] = zero ? 0.f : C * exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
