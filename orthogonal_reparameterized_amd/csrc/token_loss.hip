@@ -100,10 +100,22 @@ __device__ __forceinline__ float fadd(float a, float b) { return a + b; }
 __device__ __forceinline__ float fmax2(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ float wave_sum(float v) { return wave_all(v, 0.f, fadd); }
 __device__ __forceinline__ float wave_max(float v) { return wave_all(v, -INFINITY, fmax2); }
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp(double v) {  // 0 where the lane has no source
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v += dpp<0x111, 0xf>(v);
+  v += dpp<0x112, 0xf>(v);
+  v += dpp<0x114, 0xf>(v);
+  v += dpp<0x118, 0xf>(v);
+  v += dpp<0x142, 0xa>(v);
+  v += dpp<0x143, 0xc>(v);
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
 #pragma unroll
@@ -126,6 +138,24 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// exp and log of a few values of a row, to float32's accuracy whatever the argument's size: the whole part of the base-2
+// exponent is split off in 64 bits, the hardware's instructions see the rest only (a 64-bit library exp or log costs
+// about 100 dependent instructions, which the row's other waves would wait for).
+__device__ __forceinline__ float exp_of(double x) {
+  const double y = x * 1.4426950408889634, n = rint(y);
+  if (!(fabs(y) < 1000.0)) return y < 0 ? 0.f : y > 0 ? INFINITY : (float)y;
+  return ldexpf(exp2_fast((float)(y - n)), (int)n);
+}
+__device__ __forceinline__ double log_of(double x) {
+  if (!(x > 0)) return x == 0 ? -(double)INFINITY : (double)NAN;
+  if (x == (double)INFINITY) return x;
+  int e;
+  double m = frexp(x, &e);  // [0.5, 1)
+  if (m < 0.70710678) { m *= 2; e -= 1; }
+  const float f = (float)m;
+  return ((double)e + (double)__builtin_amdgcn_logf(f)) * 0.6931471805599453 + (double)((float)(m - (double)f) / f);
+}
 
 // ---- the order of the alternatives ----------------------------------------------------------------------------
 // larger logit first, then the lower index; NaN after everything else (o = 0). Keys of one row are distinct.
@@ -503,55 +533,69 @@ __global__ __launch_bounds__(256) void k_logprobs_join(const TokenArgs a, const 
 // in this list, so that the sum over the unlisted tokens, with its own maximum mt, needs no subtraction however little
 // they hold, and the passes over the row need no tests.
 struct List {
-  float q[POET_MAX_TOP], lq[POET_MAX_TOP], z[POET_MAX_TOP];  // teacher's probability and its logarithm; student's logit
+  double lq[POET_MAX_TOP];                // logarithm of the teacher's probability
+  float q[POET_MAX_TOP], z[POET_MAX_TOP];  // the probability; the student's logit
   int id[POET_MAX_TOP];   // -1: absent
   float all[POET_MAX_TOP];  // for an id's first entry: the sum of q over its entries; else unused
-  float qt;               // TAIL: what the list leaves
+  float qt, w;            // TAIL: what the list leaves; the row's upstream gradient
   int some, repeated;     // any entry; any id twice
   float m, logZ, mt, logZt;  // the row's statistics
   float C, scale;         // gradient: factors of the unlisted tokens, of the listed ones (grad_factors)
 };
 
-// One wave (all 64 lanes; entry k belongs to lane k % 64) loads row `row`'s list: the ids, the student's logits and, in
-// lq, the teacher's as they are. `z` is the student's row.
-template <class T> __device__ void load_list(List& L, const TokenArgs& a, int64_t row, const T* z) {
-  const int lane = threadIdx.x & 63;
-  for (int k = lane; k < a.K; k += 64) {
-    int id = a.t_ids[row * a.K + k];
-    if (id < 0 || id >= a.V) id = -1;
-    L.id[k] = id;
-    L.z[k] = id < 0 ? -INFINITY : (float)z[id];
-    L.lq[k] = id < 0 ? -INFINITY : a.t_z[row * a.K + k];
+// One wave (all 64 lanes; entry k belongs to lane k % 64) loads row `row`'s list in two steps, so that the row itself can
+// be on its way from memory between them; z is the student's row. The list's logarithms are kept in 64 bits: the loss is
+// the small difference of the teacher's and the student's.
+struct ListRaw { int id[2]; float t[2]; float lse, w; };
+__device__ __forceinline__ ListRaw fetch_list(const TokenArgs& a, int64_t row) {
+  ListRaw r;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int k = (threadIdx.x & 63) + 64 * u;
+    r.id[u] = k < a.K ? a.t_ids[row * a.K + k] : -1;
+    r.t[u] = k < a.K ? a.t_z[row * a.K + k] : -INFINITY;
   }
-  if (lane == 0) L.repeated = 0;
+  r.lse = a.t_lse ? a.t_lse[row] : 0.f;
+  r.w = a.dloss ? a.dloss[row] : 0.f;
+  return r;
 }
-
-// The teacher's probabilities from a loaded list, by the same wave. The list's few logarithms are taken in 64 bits: the
-// loss is the small difference of the teacher's and the student's.
-__device__ void teach(List& L, const TokenArgs& a, int64_t row) {
+template <class T> __device__ void teach(List& L, const TokenArgs& a, const T* z, ListRaw r) {
   const int lane = threadIdx.x & 63;
-  bool some = false, odd = false;
-  float tm = -INFINITY;
-  for (int k = lane; k < a.K; k += 64) {
-    some |= L.id[k] >= 0;
-    odd |= L.lq[k] != L.lq[k];
-    tm = fmaxf(tm, L.lq[k]);
+  float zl[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    if (r.id[u] < 0 || r.id[u] >= a.V) { r.id[u] = -1; r.t[u] = -INFINITY; }
+    zl[u] = r.id[u] < 0 ? -INFINITY : (float)z[r.id[u]];
   }
-  some = __any(some);
-  tm = wave_max(tm);
-  if (!a.tail) some = some && (tm > -INFINITY || __any(odd));  // entries at -inf are as good as absent
-  const double off = a.tail ? (a.t_lse ? (double)a.t_lse[row] : 0.0) : (double)tm * a.ts;
-  double Q = 0;
-  for (int k = lane; k < a.K; k += 64)
-    if (some && L.id[k] >= 0) Q += exp((double)L.lq[k] * a.ts - off);
+  bool some = __any(r.id[0] >= 0 || r.id[1] >= 0);
+  const float tm = wave_max(fmaxf(r.t[0], r.t[1]));
+  if (!a.tail) some = some && (tm > -INFINITY || __any(r.t[0] != r.t[0] || r.t[1] != r.t[1]));  // -inf is as good as absent
+  double l[2], Q = 0;
+  float e[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    l[u] = (double)r.t[u] * a.ts - (a.tail ? (double)r.lse : (double)tm * a.ts);
+    e[u] = some && r.id[u] >= 0 ? exp_of(l[u]) : 0.f;
+    Q += (double)e[u];
+  }
   Q = wave_sum(Q);
-  const double lQ = a.tail || !some ? off : off + log(Q);
-  for (int k = lane; k < a.K; k += 64) {
-    const double l = (double)L.lq[k] * a.ts - lQ;
-    L.lq[k] = (float)l;
-    L.q[k] = L.all[k] = some && L.id[k] >= 0 ? (float)exp(l) : 0.f;
+  const double lQ = a.tail || !some ? 0.0 : log_of(Q);
+  const float scale = a.tail || !some ? 1.f : (float)(1.0 / Q);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int k = lane + 64 * u;
+    if (k >= a.K) continue;
+    L.id[k] = r.id[u];
+    L.z[k] = zl[u];
+    L.lq[k] = l[u] - lQ;
+    L.q[k] = L.all[k] = e[u] * scale;
   }
-  if (lane == 0) { L.some = some; L.qt = a.tail && some ? fmaxf((float)(1.0 - Q), 0.f) : 0.f; }
+  if (lane == 0) {
+    L.some = some;
+    L.repeated = 0;
+    L.qt = a.tail && some ? fmaxf((float)(1.0 - Q), 0.f) : 0.f;
+    L.w = r.w;
+  }
 }
 
 // Marks the repeated ids of a list (one wave, after teach and a barrier or wave_fence): `all` of an id's first entry is the sum of
@@ -587,20 +631,19 @@ __device__ void finish_distill(List& L, const TokenArgs& a, int64_t row, float m
     if (L.id[k] >= 0) m = fmaxf(m, L.z[k]);
   m = wave_max(m);
   const float ref = m == -INFINITY ? 0.f : m;
-  const double s = a.s;
+  const double s = a.s, dt = ((double)(mt == -INFINITY ? 0.f : mt) - ref) * s;
   double Z = 0;
   for (int k = lane; k < a.K; k += 64)
-    if (stands(L, k)) Z += exp(((double)L.z[k] - ref) * s);
+    if (stands(L, k)) Z += (double)exp_of(((double)L.z[k] - ref) * s);
   Z = wave_sum(Z);
-  if (Zt != 0.0) Z += Zt * exp(((double)(mt == -INFINITY ? 0.f : mt) - ref) * s);
+  if (Zt != 0.0) Z += Zt * (double)exp_of(dt);
   const bool none = m == -INFINITY && Z == 0.0;
-  const double logZ = log(Z), logZt = log(Zt);
+  const double logZ = log_of(Z), logZt = log_of(Zt);
   double loss = 0;
   for (int k = lane; k < a.K; k += 64)
     if (L.q[k] > 0.f || L.q[k] != L.q[k]) loss += none ? INFINITY : (double)L.q[k] * (L.lq[k] - (((double)L.z[k] - ref) * s - logZ));
   loss = wave_sum(loss);
-  if (L.qt > 0.f)
-    loss += none ? INFINITY : L.qt * (log((double)L.qt) - (logZt + ((double)(mt == -INFINITY ? 0.f : mt) - ref) * s - logZ));
+  if (L.qt > 0.f) loss += none ? INFINITY : L.qt * (log_of((double)L.qt) - (logZt + dt - logZ));
   if (lane == 0) {
     a.loss[row] = L.some ? (float)loss : 0.f;
     float* q = a.stats + row * 4;
@@ -610,21 +653,21 @@ __device__ void finish_distill(List& L, const TokenArgs& a, int64_t row, float m
 
 // The gradient's factors from the row's statistics in L (one thread): unlisted tokens get C exp(s (z - mt)), listed ones
 // scale (exp(s (z - m) - log Z) - sum q).
-__device__ void grad_factors(List& L, const TokenArgs& a, int64_t row) {
-  const float w = L.some ? a.dloss[row] : 0.f;
+__device__ void grad_factors(List& L, const TokenArgs& a) {
+  const float w = L.some ? L.w : 0.f;
   const bool zero = w == 0.f || (L.m == -INFINITY && L.logZ == -INFINITY);
   const float ref = L.m == -INFINITY ? 0.f : L.m;
   float C = 0.f;
   if (!zero && L.logZt != -INFINITY) {
-    C = expf(((L.mt == -INFINITY ? 0.f : L.mt) - ref) * a.s - L.logZ);
-    if (L.qt > 0.f) C -= L.qt * expf(-L.logZt);
+    C = exp_of(((double)(L.mt == -INFINITY ? 0.f : L.mt) - ref) * a.s - L.logZ);
+    if (L.qt > 0.f) C -= L.qt * exp_of(-(double)L.logZt);
   }
   L.scale = zero ? 0.f : w * a.s;
   L.C = C * L.scale;
 }
 __device__ __forceinline__ float grad_listed(const List& L, int k, float s) {
   const float ref = L.m == -INFINITY ? 0.f : L.m;
-  return L.scale == 0.f ? 0.f : L.scale * (expf((L.z[k] - ref) * s - L.logZ) - L.all[k]);
+  return L.scale == 0.f ? 0.f : L.scale * (exp_of(((double)L.z[k] - ref) * s - L.logZ) - L.all[k]);
 }
 
 // One workgroup a row or segment, as k_logprobs; partials: mt, Zt.
@@ -641,10 +684,12 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
     const T* z = (const T*)a.z + row * a.ld;
     const int n = min(sp.len, a.V - base);
     const Steps<T> s(z + base, n);
+    ListRaw raw;
+    if (wave == 0) raw = fetch_list(a, row);
     Held<T, NT, VPT> h;
     h.load(s);
     for (int i = tid; i <= NT * VPT / 4; i += NT) bits[i] = 0;
-    if (wave == 0) load_list<T>(L, a, row, z);
+    if (wave == 0) teach<T>(L, a, z, raw);
     __syncthreads();
     if (wave == 0) {
       bool twice = false;
@@ -702,12 +747,9 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
     if (wave == 0) {
       double Zt = 0;
       for (int q = 0; q < NT / 64; ++q) Zt += sz[q];
-      teach(L, a, row);
-      wave_fence();
       if (L.repeated) join_repeated(L, a.K);
-      wave_fence();
       finish_distill(L, a, row, mt, Zt);
-      if (a.dz && lane == 0) grad_factors(L, a, row);
+      if (a.dz && lane == 0) grad_factors(L, a);
     }
     __syncthreads();
     if (a.dz) {
@@ -738,9 +780,7 @@ template <class T> __global__ __launch_bounds__(64) void k_distill_join(const To
   __shared__ List L;
   const int lane = threadIdx.x;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-    load_list<T>(L, a, row, (const T*)a.z + row * a.ld);
-    __syncthreads();
-    teach(L, a, row);
+    teach<T>(L, a, (const T*)a.z + row * a.ld, fetch_list(a, row));
     __syncthreads();
     join_repeated(L, a.K);
     __syncthreads();
@@ -774,9 +814,10 @@ template <class T> __device__ __forceinline__ void put_step(const Steps<T>& s, T
 
 template <class T>
 __global__ __launch_bounds__(kGradThreads) void k_logprobs_bwd(const TokenArgs a, int chunks, int len) {
-  for (int64_t w = blockIdx.x; w < (int64_t)a.T * chunks; w += gridDim.x) {
-    const int64_t row = w / chunks;
-    const int base = (int)(w - row * chunks) * len;
+  const int64_t total = (int64_t)a.T * chunks;
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    const int64_t at = total - 1 - w, row = at / chunks;  // last rows first: they are the nearest in the caches
+    const int base = (int)(at - row * chunks) * len;
     const T* z = (const T*)a.z + row * a.ld;
     T* dz = (T*)a.dz + row * a.ldd;
     const int n = min(len, a.V - base);
@@ -809,61 +850,65 @@ template <class T>
 __global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a, int chunks, int len) {
   __shared__ List L;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t w = blockIdx.x; w < (int64_t)a.T * chunks; w += gridDim.x) {
-    const int64_t row = w / chunks;
-    const int base = (int)(w - row * chunks) * len;
+  const int64_t total = (int64_t)a.T * chunks;
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    const int64_t at = total - 1 - w, row = at / chunks;  // last rows first: they are the nearest in the caches
+    const int base = (int)(at - row * chunks) * len, end = min(len, a.V - base);
     const T* z = (const T*)a.z + row * a.ld;
     T* dz = (T*)a.dz + row * a.ldd;
-    const int n = min(len, a.V - base);
-    const Steps<T> s(z + base, n);
-    Held<T, kGradThreads, kGradSteps> h;
-    h.load(s);
     const float* q = a.stats + row * 4;
     const float ref = q[2] == -INFINITY ? 0.f : q[2], c = a.s * kLog2e;
     // the listed logits are read here, before this workgroup's steps may overwrite them in place; another workgroup
     // may have overwritten those outside this chunk, which are not used
-    if (wave == 0) load_list<T>(L, a, row, z);
-    __syncthreads();
     if (wave == 0) {
-      teach(L, a, row);
+      teach<T>(L, a, z, fetch_list(a, row));
       wave_fence();
       join_repeated(L, a.K);
       if (lane == 0) {
         L.m = q[0]; L.logZ = q[1]; L.mt = q[2]; L.logZt = q[3];
-        grad_factors(L, a, row);
+        grad_factors(L, a);
       }
     }
     __syncthreads();
     const bool wide = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     const float C = L.C;
     const bool zero = L.scale == 0.f;
-    dz += base;
+    constexpr int kTile = kGradThreads * kGradSteps * Vec<T>::N;
+    for (int b = 0; b < end; b += kTile) {
+      const Steps<T> s(z + base + b, min(kTile, end - b));
+      Held<T, kGradThreads, kGradSteps> h;
+      h.load(s);
+      T* out = dz + base + b;
 #pragma unroll
-    for (int i = 0; i < kGradSteps; ++i) {
-      const int v = threadIdx.x + i * kGradThreads;
-      float f[Vec<T>::N];
+      for (int i = 0; i < kGradSteps; ++i) {
+        const int v = threadIdx.x + i * kGradThreads;
+        float f[Vec<T>::N];
 #pragma unroll
-      for (int k = 0; k < Vec<T>::N; ++k) f[k] = zero ? 0.f : C * exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
-      if (v < s.steps) put_step(s, dz, wide, v, f);
+        for (int k = 0; k < Vec<T>::N; ++k) f[k] = zero ? 0.f : C * exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
+        if (v < s.steps) put_step(s, out, wide, v, f);
+      }
+      if ((int)threadIdx.x < s.singles) out[s.single(threadIdx.x)] = (T)(zero ? 0.f : C * exp2_fast((h.x - ref) * c));
     }
-    if ((int)threadIdx.x < s.singles) dz[s.single(threadIdx.x)] = (T)(zero ? 0.f : C * exp2_fast((h.x - ref) * c));
     __syncthreads();
     if (wave == 0)
       for (int k = lane; k < a.K; k += 64)
-        if (stands(L, k) && L.id[k] >= base && L.id[k] < base + n) dz[L.id[k] - base] = (T)grad_listed(L, k, a.s);
+        if (stands(L, k) && L.id[k] >= base && L.id[k] < base + end) dz[L.id[k]] = (T)grad_listed(L, k, a.s);
     __syncthreads();
   }
 }
 
 // ---- launches ----------------------------------------------------------------------------------------------------
-constexpr int kHeld = 1024 * 16;  // steps that the largest workgroup holds
+constexpr int kHeld = 1024 * 16;    // steps that the largest workgroup holds
+constexpr int kSegment = 256 * 16;  // ... and that the largest of 256 threads holds, four of which share a CU
 
-// How rows of V elements are split (a row of at most N-1 elements more than a workgroup's steps goes with those as its
-// single elements, however it is aligned)
-RowSplit split_of(int V, int dt, int K) {
-  const int n = dt == BF16 ? 8 : 4, cap = kHeld * n;
+// How rows of V elements are split over workgroups of `held` steps (a row of at most N-1 elements more than a workgroup's
+// steps goes with those as its single elements, however it is aligned). With its gradient a row stays whole where it can,
+// to be read once (and wherever the gradient is written, so that it is the same); without, segments keep more loads in
+// flight.
+RowSplit split_of(int V, int dt, int K, bool grad) {
+  const int n = dt == BF16 ? 8 : 4, held = grad ? kHeld : kSegment, cap = held * n;
   RowSplit sp;
-  if (V / n > kHeld) sp.nseg = (V + cap - 1) / cap;
+  if (V / n > held) sp.nseg = (V + cap - 1) / cap;
   sp.len = sp.nseg == 1 ? V : ((V + sp.nseg - 1) / sp.nseg + 63) / 64 * 64;  // <= cap, and whole steps
   sp.stride = 4 + 2 * K;
   sp.steps = sp.len / n;
@@ -897,15 +942,15 @@ template <class F> hipError_t by_type(int dt, F f) {
 }  // namespace
 
 size_t logprobs_part_bytes(int T, int V, int dt, int K) {
-  const RowSplit sp = split_of(V, dt, K);
+  const RowSplit sp = split_of(V, dt, K, false);
   return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
 
 hipError_t launch_logprobs(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  RowSplit sp = split_of(a.V, a.dt, a.K);
+  const bool after = a.dz && (a.V / (a.dt == BF16 ? 8 : 4) > kHeld || !same_alignment(a));  // the gradient in its own launch
+  RowSplit sp = split_of(a.V, a.dt, a.K, a.dz);
   sp.part = part;
-  const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in a launch of its own
   if (after) a.dz = nullptr;
   {
     const double e = dtype_size(a.dt), n = (double)a.T * a.V;
@@ -936,15 +981,15 @@ hipError_t launch_logprobs_bwd(const TokenArgs& a, hipStream_t st) {
 }
 
 size_t distill_part_bytes(int T, int V, int dt) {
-  const RowSplit sp = split_of(V, dt, 0);
+  const RowSplit sp = split_of(V, dt, 0, false);
   return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
 
 hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  RowSplit sp = split_of(a.V, a.dt, 0);
+  const bool after = a.dz && (a.V / (a.dt == BF16 ? 8 : 4) > kHeld || !same_alignment(a));  // the gradient in its own launch
+  RowSplit sp = split_of(a.V, a.dt, 0, a.dz);
   sp.part = part;
-  const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in a launch of its own
   if (after) a.dz = nullptr;
   {
     const double e = dtype_size(a.dt), n = (double)a.T * a.V;
@@ -966,7 +1011,11 @@ hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
 }
 
 hipError_t launch_distill_bwd(const TokenArgs& a, hipStream_t st) {
-  const int n = a.dt == BF16 ? 8 : 4, len = kGradThreads * kGradSteps * n, chunks = (a.V + len - 1) / len;
+  // a workgroup reads its row's list once for several tiles, while there are workgroups enough
+  const int tile = kGradThreads * kGradSteps * (a.dt == BF16 ? 8 : 4);
+  const int64_t tiles = (a.V + tile - 1) / tile;
+  const int len = tile * (int)std::min<int64_t>(16, std::max<int64_t>(1, tiles * a.T / 4096));
+  const int chunks = (a.V + len - 1) / len;
   ProfScope prof(POET_K_HEAD, st, 4.0 * a.T * a.V, 2.0 * a.T * a.V * dtype_size(a.dt));
   return by_type(a.dt, [&](auto t) {
     hipLaunchKernelGGL(k_distill_bwd<decltype(t)>, grid_of((int64_t)a.T * chunks), dim3(kGradThreads), 0, st, a, chunks, len);
