@@ -619,6 +619,19 @@ __device__ void join_repeated(List& L, int K) {
     if (lane + 64 * u < K) L.all[lane + 64 * u] = sum[u];
 }
 
+// Whether an id of the list appears twice (one wave, from the ids that teach() left): each id against all, in registers
+__device__ bool any_repeated(const List& L, int K) {
+  const int lane = threadIdx.x & 63;
+  const int i0 = lane < K ? L.id[lane] : -1, i1 = lane + 64 < K ? L.id[lane + 64] : -1;
+  int n0 = 0, n1 = 0;
+  for (int o = 0; o < K; ++o) {
+    const int id = __builtin_amdgcn_readlane(o < 64 ? i0 : i1, o & 63);
+    n0 += i0 == id;
+    n1 += i1 == id;
+  }
+  return __any((i0 >= 0 && n0 > 1) || (i1 >= 0 && n1 > 1));
+}
+
 // An entry that stands for its token in sums over distinct tokens and in the gradient
 __device__ __forceinline__ bool stands(const List& L, int k) { return L.id[k] >= 0 && L.all[k] >= 0.f; }
 
@@ -781,9 +794,8 @@ template <class T> __global__ __launch_bounds__(64) void k_distill_join(const To
   const int lane = threadIdx.x;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     teach<T>(L, a, (const T*)a.z + row * a.ld, fetch_list(a, row));
-    __syncthreads();
-    join_repeated(L, a.K);
-    __syncthreads();
+    wave_fence();
+    if (any_repeated(L, a.K)) join_repeated(L, a.K);
     const float* part = sp.part + row * sp.nseg * sp.stride;
     float mt = -INFINITY;
     for (int q = lane; q < sp.nseg; q += 64) mt = fmaxf(mt, part[q * sp.stride]);
@@ -858,12 +870,15 @@ __global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a,
     T* dz = (T*)a.dz + row * a.ldd;
     const float* q = a.stats + row * 4;
     const float ref = q[2] == -INFINITY ? 0.f : q[2], c = a.s * kLog2e;
+    constexpr int kTile = kGradThreads * kGradSteps * Vec<T>::N;
+    Held<T, kGradThreads, kGradSteps> h, next;
+    h.load(Steps<T>(z + base, min(kTile, end)));
     // the listed logits are read here, before this workgroup's steps may overwrite them in place; another workgroup
     // may have overwritten those outside this chunk, which are not used
     if (wave == 0) {
       teach<T>(L, a, z, fetch_list(a, row));
       wave_fence();
-      join_repeated(L, a.K);
+      if (any_repeated(L, a.K)) join_repeated(L, a.K);
       if (lane == 0) {
         L.m = q[0]; L.logZ = q[1]; L.mt = q[2]; L.logZt = q[3];
         grad_factors(L, a);
@@ -873,11 +888,9 @@ __global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a,
     const bool wide = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     const float C = L.C;
     const bool zero = L.scale == 0.f;
-    constexpr int kTile = kGradThreads * kGradSteps * Vec<T>::N;
-    for (int b = 0; b < end; b += kTile) {
+    for (int b = 0; b < end; b += kTile, h = next) {
       const Steps<T> s(z + base + b, min(kTile, end - b));
-      Held<T, kGradThreads, kGradSteps> h;
-      h.load(s);
+      if (b + kTile < end) next.load(Steps<T>(z + base + b + kTile, min(kTile, end - b - kTile)));
       T* out = dz + base + b;
 #pragma unroll
       for (int i = 0; i < kGradSteps; ++i) {
@@ -906,7 +919,7 @@ constexpr int kSegment = 256 * 16;  // ... and that the largest of 256 threads h
 // to be read once (and wherever the gradient is written, so that it is the same); without, segments keep more loads in
 // flight.
 RowSplit split_of(int V, int dt, int K, bool grad) {
-  const int n = dt == BF16 ? 8 : 4, held = grad ? kHeld : kSegment, cap = held * n;
+  const int n = dt == BF16 ? 8 : 4, held = grad && V / n <= kHeld ? kHeld : kSegment, cap = held * n;
   RowSplit sp;
   if (V / n > held) sp.nseg = (V + cap - 1) / cap;
   sp.len = sp.nseg == 1 ? V : ((V + sp.nseg - 1) / sp.nseg + 63) / 64 * 64;  // <= cap, and whole steps
@@ -949,7 +962,7 @@ size_t logprobs_part_bytes(int T, int V, int dt, int K) {
 hipError_t launch_logprobs(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
   const bool after = a.dz && (a.V / (a.dt == BF16 ? 8 : 4) > kHeld || !same_alignment(a));  // the gradient in its own launch
-  RowSplit sp = split_of(a.V, a.dt, a.K, a.dz);
+  RowSplit sp = split_of(a.V, a.dt, a.K, args.dz);
   sp.part = part;
   if (after) a.dz = nullptr;
   {
@@ -988,7 +1001,7 @@ size_t distill_part_bytes(int T, int V, int dt) {
 hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
   const bool after = a.dz && (a.V / (a.dt == BF16 ? 8 : 4) > kHeld || !same_alignment(a));  // the gradient in its own launch
-  RowSplit sp = split_of(a.V, a.dt, 0, a.dz);
+  RowSplit sp = split_of(a.V, a.dt, 0, args.dz);
   sp.part = part;
   if (after) a.dz = nullptr;
   {
