@@ -325,9 +325,15 @@ def poet_profile_query(kclass: int) -> dict:
 
 # ---- marshalling -------------------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dt_name(dt: int) -> str:
@@ -757,29 +763,58 @@ def poet_singular_value_entropy(m: int, n: int, W, ldw: int, entropy, sigma=None
 
 # ---- the model's answer: token log-probabilities and distillation --------------------------------------------
 # Logits and their gradient are 2-D device tensors of float32 or bfloat16 with unit column stride and any row stride;
-# every tensor of a call lives on the current device.
+# every tensor of a call lives on the current device. These calls are made for single tokens too, where the time on the
+# host counts: one look at the device and the stream a call, and no work where an optional tensor is absent.
 
-def _on_device(t, name: str, dtype: str):
-    """t is a torch tensor of the given dtype(s) on the current device."""
+_TYPES = {}  # torch dtype -> (name, the library's dtype or None); filled at the first use
+
+
+def _types() -> dict:
+    if not _TYPES:
+        torch = _torch()
+        _TYPES.update({torch.float32: ("float32", POET_F32), torch.bfloat16: ("bfloat16", POET_BF16),
+                       torch.int32: ("int32", None)})
+    return _TYPES
+
+
+def _device_of(t, name: str) -> int:
+    """The device of a call: that of its main tensor, which must be the current one."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    dt = str(t.dtype)[6:]
-    if dt not in dtype.split("|"):
-        raise TypeError(f"{name} must be {dtype.replace('|', ' or ')}, got {t.dtype}")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _refuse(t, name: str, dev: int):
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    raise ValueError(f"{name} must be a GPU tensor on cuda:{dev}, got {t.device}")
+
+
+def _dtype_of(t, name: str):
+    """The library's dtype of a matrix of logits, activations or residuals."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    dt = _types().get(t.dtype, (None, None))[1]
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     return dt
 
 
-def _mat(t, name: str, rows: int, cols: int, dtype: str):
+def _mat(t, name: str, rows: int, cols: int, dtype, dev: int):
     """(device pointer, row pitch in elements) of a rows x cols tensor with unit column stride; None: (None, 0)."""
     if t is None:
         return None, 0
-    _on_device(t, name, dtype)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if not isinstance(t, _torch().Tensor) or t.get_device() != dev:
+        _refuse(t, name, dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
     ld, unit = t.stride()
     if (cols > 1 and unit != 1) or (rows > 1 and ld < cols):
@@ -787,44 +822,56 @@ def _mat(t, name: str, rows: int, cols: int, dtype: str):
     return t.data_ptr(), ld if rows > 1 else max(ld, cols)
 
 
-def _vec(t, name: str, shape: tuple, dtype: str, required: bool = False):
+def _vec(t, name: str, shape: tuple, dtype, dev: int, required: bool = False):
     """Device pointer of a contiguous tensor of exactly this shape (None where it is optional)."""
     if t is None:
         if required:
             raise ValueError(f"{name} is required")
         return None
-    _on_device(t, name, dtype)
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if not isinstance(t, _torch().Tensor) or t.get_device() != dev:
+        _refuse(t, name, dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {shape}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _scratch(ws, need: int, like, stream):
-    """(pointer, bytes) of the workspace; taken from torch on the current stream when the caller keeps none."""
-    if ws is None:
-        if need == 0:
-            return None, 0, None
-        if stream is not None:
-            raise ValueError(f"a call on a stream of its own needs ws ({need} bytes): memory from torch would be "
-                             "reused by the current stream")
-        ws = _torch().empty(need, dtype=_torch().uint8, device=like.device)
-    else:
-        _on_device(ws, "ws", str(ws.dtype)[6:])
+def _scratch(ws, need, dev: int, stream):
+    """(pointer, bytes, tensor) of the workspace; need() bytes are taken from torch on the current stream when the
+    caller keeps none (the library checks the size of a kept one)."""
+    if ws is not None:
+        if not isinstance(ws, _torch().Tensor) or ws.get_device() != dev:
+            _refuse(ws, "ws", dev)
         if not ws.is_contiguous():
             raise ValueError("ws must be contiguous")
-    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+        return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+    need = need()
+    if need == 0:
+        return None, 0, None
+    if stream is not None:
+        raise ValueError(f"a call on a stream of its own needs ws ({need} bytes): memory from torch would be "
+                         "reused by the current stream")
+    ws = _torch().empty(need, dtype=_torch().uint8, device=f"cuda:{dev}")
+    return ws.data_ptr(), need, ws
+
+
+def _on_stream(stream, dev: int):
+    """The HIP stream handle of a call on device dev: the current stream's where none is given."""
+    if stream is not None:
+        return _stream(stream)
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else _stream(None)
 
 
 def _logits(logits, inv_temp: float):
     if logits is None or logits.dim() != 2:
         raise ValueError("logits must be a 2-D tensor")
+    dt = _dtype_of(logits, "logits")
+    dev = _device_of(logits, "logits")
     T, V = logits.shape
-    p, ld = _mat(logits, "logits", T, V, "float32|bfloat16")
-    return p, poet_logits(T, V, ld, POET_F32 if logits.dtype is _torch().float32 else POET_BF16, inv_temp)
-
-
-def _grad(dlogits, logits):
-    return _mat(dlogits, "dlogits", logits.shape[0], logits.shape[1], str(logits.dtype)[6:])
+    p, ld = _mat(logits, "logits", T, V, logits.dtype, dev)
+    return p, poet_logits(T, V, ld, dt, inv_temp), T, V, dev
 
 
 def poet_token_logprobs_workspace_bytes(T: int, V: int, dtype: int, K: int) -> int:
@@ -836,94 +883,99 @@ def poet_token_logprobs(logits, ids, logp, stats, inv_temp: float = 1.0, entropy
     """Per row of logits [T, V] (float32 or bf16): logp [T] = log p[ids] (ids int32; outside [0, V): 0), entropy [T],
     the K best alternatives top_ids [T, K] int32 / top_logp [T, K], stats [T, 4] for the backward (all float32; None
     leaves one out, ids and logp together). With dlogp and / or dentropy [T] known beforehand, dlogits [T, V] too."""
-    z, L = _logits(logits, inv_temp)
-    T, V = L.T, L.V
+    z, L, T, V, dev = _logits(logits, inv_temp)
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
     K = 0 if top_ids is None else top_ids.shape[-1]
-    need = poet_token_logprobs_workspace_bytes(T, V, L.dtype, K)
-    dz, ldd = _grad(dlogits, logits)
-    wp, wn, ws = _scratch(ws, need, logits, stream)
+    dz, ldd = _mat(dlogits, "dlogits", T, V, logits.dtype, dev)
+    wp, wn, ws = _scratch(ws, lambda: poet_token_logprobs_workspace_bytes(T, V, L.dtype, K), dev, stream)
     st = lib().poet_token_logprobs(
-        ctypes.byref(L), z, _vec(ids, "ids", (T,), "int32"), K, _vec(dlogp, "dlogp", (T,), "float32"),
-        _vec(dentropy, "dentropy", (T,), "float32"), _vec(logp, "logp", (T,), "float32"),
-        _vec(entropy, "entropy", (T,), "float32"), _vec(top_ids, "top_ids", (T, K), "int32"),
-        _vec(top_logp, "top_logp", (T, K), "float32"), _vec(stats, "stats", (T, 4), "float32", True), dz, ldd, wp, wn,
-        _stream(stream))
-    _check(st, "poet_token_logprobs")
+        ctypes.byref(L), z, _vec(ids, "ids", (T,), i32, dev), K, _vec(dlogp, "dlogp", (T,), f32, dev),
+        _vec(dentropy, "dentropy", (T,), f32, dev), _vec(logp, "logp", (T,), f32, dev),
+        _vec(entropy, "entropy", (T,), f32, dev), _vec(top_ids, "top_ids", (T, K), i32, dev),
+        _vec(top_logp, "top_logp", (T, K), f32, dev), _vec(stats, "stats", (T, 4), f32, dev, True), dz, ldd, wp, wn,
+        _on_stream(stream, dev))
+    if st:
+        _check(st, "poet_token_logprobs")
 
 
 def poet_token_logprobs_bwd(logits, ids, stats, dlogp, dlogits, inv_temp: float = 1.0, dentropy=None, stream=None):
     """The logits' gradient after poet_token_logprobs (its stats; the same logits, ids and inv_temp), for upstream
     gradients dlogp and / or dentropy [T] that depend on its results. dlogits may be the logits (in place)."""
-    z, L = _logits(logits, inv_temp)
-    T = L.T
-    dz, ldd = _grad(dlogits, logits)
+    z, L, T, V, dev = _logits(logits, inv_temp)
+    torch = _torch()
+    f32 = torch.float32
+    dz, ldd = _mat(dlogits, "dlogits", T, V, logits.dtype, dev)
     st = lib().poet_token_logprobs_bwd(
-        ctypes.byref(L), z, _vec(ids, "ids", (T,), "int32"), _vec(stats, "stats", (T, 4), "float32", True),
-        _vec(dlogp, "dlogp", (T,), "float32"), _vec(dentropy, "dentropy", (T,), "float32"), dz, ldd, _stream(stream))
-    _check(st, "poet_token_logprobs_bwd")
+        ctypes.byref(L), z, _vec(ids, "ids", (T,), torch.int32, dev), _vec(stats, "stats", (T, 4), f32, dev, True),
+        _vec(dlogp, "dlogp", (T,), f32, dev), _vec(dentropy, "dentropy", (T,), f32, dev), dz, ldd, _on_stream(stream, dev))
+    if st:
+        _check(st, "poet_token_logprobs_bwd")
 
 
 def poet_distill_workspace_bytes(T: int, V: int, dtype: int) -> int:
     return int(lib().poet_distill_workspace_bytes(T, V, dtype))
 
 
-def _teacher(t_ids, t_logits, t_lse, mode, t_inv_temp, T):
+def _teacher(t_ids, t_logits, t_lse, mode, t_inv_temp, T, dev):
     if t_ids is None or t_ids.dim() != 2:
         raise ValueError("t_ids must be a 2-D tensor")
-    K = t_ids.shape[1]
-    return poet_teacher(K, mode, t_inv_temp), _vec(t_ids, "t_ids", (T, K), "int32"), \
-        _vec(t_logits, "t_logits", (T, K), "float32", True), _vec(t_lse, "t_lse", (T,), "float32")
+    K, f32 = t_ids.shape[1], _torch().float32
+    return poet_teacher(K, mode, t_inv_temp), _vec(t_ids, "t_ids", (T, K), _torch().int32, dev), \
+        _vec(t_logits, "t_logits", (T, K), f32, dev, True), _vec(t_lse, "t_lse", (T,), f32, dev)
 
 
-def poet_distill(logits, t_ids, t_logits, loss, stats, mode: int = 0, inv_temp: float = 1.0, t_inv_temp: float = 1.0,
-                 t_lse=None, dloss=None, dlogits=None, ws=None, stream=None):
+def poet_distill(logits, t_ids, t_logits, loss, stats, mode: int = POET_DISTILL_RENORM, inv_temp: float = 1.0,
+                 t_inv_temp: float = 1.0, t_lse=None, dloss=None, dlogits=None, ws=None, stream=None):
     """loss [T] float32: the divergence of each row of logits [T, V] from a teacher given by its top logits t_ids
     [T, K] int32, t_logits [T, K] float32 (mode POET_DISTILL_RENORM or POET_DISTILL_TAIL, with t_lse [T]); stats [T, 4]
     for the backward. With the rows' upstream gradients dloss [T] known beforehand, dlogits [T, V] too."""
-    z, L = _logits(logits, inv_temp)
-    T = L.T
-    teacher, ti, tz, tl = _teacher(t_ids, t_logits, t_lse, mode, t_inv_temp, T)
-    dz, ldd = _grad(dlogits, logits)
-    wp, wn, ws = _scratch(ws, poet_distill_workspace_bytes(T, L.V, L.dtype), logits, stream)
-    st = lib().poet_distill(ctypes.byref(L), ctypes.byref(teacher), z, ti, tz, tl, _vec(dloss, "dloss", (T,), "float32"),
-                            _vec(loss, "loss", (T,), "float32", True), _vec(stats, "stats", (T, 4), "float32", True),
-                            dz, ldd, wp, wn, _stream(stream))
-    _check(st, "poet_distill")
+    z, L, T, V, dev = _logits(logits, inv_temp)
+    f32 = _torch().float32
+    teacher, ti, tz, tl = _teacher(t_ids, t_logits, t_lse, mode, t_inv_temp, T, dev)
+    dz, ldd = _mat(dlogits, "dlogits", T, V, logits.dtype, dev)
+    wp, wn, ws = _scratch(ws, lambda: poet_distill_workspace_bytes(T, V, L.dtype), dev, stream)
+    st = lib().poet_distill(ctypes.byref(L), ctypes.byref(teacher), z, ti, tz, tl, _vec(dloss, "dloss", (T,), f32, dev),
+                            _vec(loss, "loss", (T,), f32, dev, True), _vec(stats, "stats", (T, 4), f32, dev, True),
+                            dz, ldd, wp, wn, _on_stream(stream, dev))
+    if st:
+        _check(st, "poet_distill")
 
 
-def poet_distill_bwd(logits, t_ids, t_logits, stats, dloss, dlogits, mode: int = 0, inv_temp: float = 1.0,
-                     t_inv_temp: float = 1.0, t_lse=None, stream=None):
+def poet_distill_bwd(logits, t_ids, t_logits, stats, dloss, dlogits, mode: int = POET_DISTILL_RENORM,
+                     inv_temp: float = 1.0, t_inv_temp: float = 1.0, t_lse=None, stream=None):
     """The logits' gradient after poet_distill (its stats; otherwise the same arguments). dlogits may be the logits."""
-    z, L = _logits(logits, inv_temp)
-    T = L.T
-    teacher, ti, tz, tl = _teacher(t_ids, t_logits, t_lse, mode, t_inv_temp, T)
-    dz, ldd = _grad(dlogits, logits)
+    z, L, T, V, dev = _logits(logits, inv_temp)
+    f32 = _torch().float32
+    teacher, ti, tz, tl = _teacher(t_ids, t_logits, t_lse, mode, t_inv_temp, T, dev)
+    dz, ldd = _mat(dlogits, "dlogits", T, V, logits.dtype, dev)
     st = lib().poet_distill_bwd(ctypes.byref(L), ctypes.byref(teacher), z, ti, tz, tl,
-                                _vec(stats, "stats", (T, 4), "float32", True),
-                                _vec(dloss, "dloss", (T,), "float32", True), dz, ldd, _stream(stream))
-    _check(st, "poet_distill_bwd")
+                                _vec(stats, "stats", (T, 4), f32, dev, True),
+                                _vec(dloss, "dloss", (T,), f32, dev, True), dz, ldd, _on_stream(stream, dev))
+    if st:
+        _check(st, "poet_distill_bwd")
 
 
 # ---- the seam between two blocks of linears -------------------------------------------------------------------
 
-def _pitch(kind: str, pairs):
-    """The one row pitch of the given (pointer, pitch) pairs; their tensors must agree in it."""
-    lds = {ld for p, ld in pairs if p is not None}
-    if len(lds) > 1:
-        raise ValueError(f"{kind} must have one row stride, got {sorted(lds)}")
-    return lds.pop() if lds else 0
+def _pitch(T: int, kind: str, *mats) -> int:
+    """The one row pitch of tensors given as (pointer, pitch) (of one row, any pitch will do)."""
+    ld = 0
+    for p, x in mats:
+        if p is None:
+            continue
+        if ld and x != ld and T > 1:
+            raise ValueError(f"{kind} must have one row stride, got {ld} and {x}")
+        ld = max(ld, x)
+    return ld
 
 
-def _norm_desc(T, d, hs, ys, gs, xs, res, act, gate_tokens, res_scale, eps):
-    # T == 1: any pitch describes one row
-    one = (lambda kind, pairs: max([ld for _, ld in pairs])) if T == 1 else _pitch
-    return poet_norm(T, d, one("h, h_out, dh_out and dh", hs), one("y and dy", ys), _pitch("gate and dgate", gs)
-                     if gs[0][0] is None or T > 1 else max(ld for _, ld in gs), one("x or dx", xs), res, act,
-                     gate_tokens, res_scale, eps)
-
-
-def _dt_of(t) -> int:
-    return POET_F32 if t.dtype is _torch().float32 else POET_BF16
+def _gate_rows(gate, T: int, gate_tokens: int) -> int:
+    if gate is None:
+        return 0
+    if gate_tokens < 1:
+        raise ValueError("gate_tokens must be >= 1")
+    return -(-T // gate_tokens)
 
 
 def poet_block_norm_fwd(h, rstd, y=None, gate=None, w_post=None, w_pre=None, h_out=None, x=None,
@@ -934,22 +986,22 @@ def poet_block_norm_fwd(h, rstd, y=None, gate=None, w_post=None, w_pre=None, h_o
     added as it is; without w_pre and x (last seam) there is no second norm. h_out may be h."""
     if h is None or h.dim() != 2:
         raise ValueError("h must be a 2-D tensor")
-    T, d = h.shape
-    res = str(h.dtype)[6:]
     a = y if y is not None else x
     if a is None:
         raise ValueError("nothing to compute: neither y nor x")
-    act = str(a.dtype)[6:]
-    if gate is not None and gate_tokens < 1:
-        raise ValueError("gate_tokens must be >= 1")
-    hp, op = _mat(h, "h", T, d, "float32|bfloat16"), _mat(h_out, "h_out", T, d, res)
-    yp, xp = _mat(y, "y", T, d, "float32|bfloat16"), _mat(x, "x", T, d, "float32|bfloat16" if y is None else act)
-    gp = _mat(gate, "gate", -(-T // gate_tokens) if gate is not None else 0, d, act)
-    N = _norm_desc(T, d, (hp, op), (yp,), (gp,), (xp,), _dt_of(h), _dt_of(a), gate_tokens, res_scale, eps)
+    T, d = h.shape
+    rows = _gate_rows(gate, T, gate_tokens)
+    res, act, dev = _dtype_of(h, "h"), _dtype_of(a, "y" if y is not None else "x"), _device_of(h, "h")
+    tr, ta, f32 = h.dtype, a.dtype, _torch().float32
+    hp, op = _mat(h, "h", T, d, tr, dev), _mat(h_out, "h_out", T, d, tr, dev)
+    yp, xp = _mat(y, "y", T, d, ta, dev), _mat(x, "x", T, d, ta, dev)
+    gp = _mat(gate, "gate", rows, d, ta, dev)
+    N = poet_norm(T, d, _pitch(T, "h and h_out", hp, op), yp[1], gp[1], xp[1], res, act, gate_tokens, res_scale, eps)
     st = lib().poet_block_norm_fwd(
-        ctypes.byref(N), hp[0], yp[0], gp[0], _vec(w_post, "w_post", (d,), "float32"),
-        _vec(w_pre, "w_pre", (d,), "float32"), op[0], xp[0], _vec(rstd, "rstd", (T, 2), "float32", True), _stream(stream))
-    _check(st, "poet_block_norm_fwd")
+        ctypes.byref(N), hp[0], yp[0], gp[0], _vec(w_post, "w_post", (d,), f32, dev), _vec(w_pre, "w_pre", (d,), f32, dev),
+        op[0], xp[0], _vec(rstd, "rstd", (T, 2), f32, dev, True), _on_stream(stream, dev))
+    if st:
+        _check(st, "poet_block_norm_fwd")
 
 
 def poet_block_norm_workspace_bytes(T: int, d: int, gate_tokens: int = 0) -> int:
@@ -966,26 +1018,24 @@ def poet_block_norm_bwd(h_out, rstd, y=None, gate=None, w_post=None, w_pre=None,
     if dh is None or dh.dim() != 2:
         raise ValueError("dh must be a 2-D tensor")
     T, d = dh.shape
-    res = str(dh.dtype)[6:]
-    a = next((t for t in (y, dy, dx) if t is not None), None)
-    act = "float32|bfloat16" if a is None else str(a.dtype)[6:]
-    if gate is not None and gate_tokens < 1:
-        raise ValueError("gate_tokens must be >= 1")
-    both = "float32|bfloat16"
-    if a is not None:
-        _on_device(a, "y, dy or dx", both)
-    hp, gh, oh = _mat(h_out, "h_out", T, d, res), _mat(dh_out, "dh_out", T, d, res), _mat(dh, "dh", T, d, both)
-    yp, gy, gx = _mat(y, "y", T, d, act), _mat(dy, "dy", T, d, act), _mat(dx, "dx", T, d, act)
-    rows = -(-T // gate_tokens) if gate is not None else 0
-    gp, gg = _mat(gate, "gate", rows, d, act), _mat(dgate, "dgate", rows, d, act)
-    N = _norm_desc(T, d, (hp, gh, oh), (yp, gy), (gp, gg), (gx,), _dt_of(dh), POET_F32 if a is None else _dt_of(a),
-                   gate_tokens, res_scale, 1.0)
-    wp, wn, ws = _scratch(ws, poet_block_norm_workspace_bytes(T, d, gate_tokens if gate is not None else 0), dh, stream)
-    f32 = lambda t, nm, shape=(d,): _vec(t, nm, shape, "float32")  # noqa: E731
+    rows = _gate_rows(gate, T, gate_tokens)
+    res, dev, f32 = _dtype_of(dh, "dh"), _device_of(dh, "dh"), _torch().float32
+    a = y if y is not None else dy if dy is not None else dx
+    act, ta = (POET_F32, None) if a is None else (_dtype_of(a, "y, dy or dx"), a.dtype)
+    tr = dh.dtype
+    hp, gh, oh = _mat(h_out, "h_out", T, d, tr, dev), _mat(dh_out, "dh_out", T, d, tr, dev), _mat(dh, "dh", T, d, tr, dev)
+    yp, gy, gx = _mat(y, "y", T, d, ta, dev), _mat(dy, "dy", T, d, ta, dev), _mat(dx, "dx", T, d, ta, dev)
+    gp, gg = _mat(gate, "gate", rows, d, ta, dev), _mat(dgate, "dgate", rows, d, ta, dev)
+    N = poet_norm(T, d, _pitch(T, "h_out, dh_out and dh", hp, gh, oh), _pitch(T, "y and dy", yp, gy),
+                  _pitch(rows, "gate and dgate", gp, gg), gx[1], res, act, gate_tokens, res_scale, 1.0)
+    wp, wn, ws = _scratch(ws, lambda: poet_block_norm_workspace_bytes(T, d, gate_tokens if gate is not None else 0), dev,
+                          stream)
     st = lib().poet_block_norm_bwd(
-        ctypes.byref(N), hp[0], yp[0], gp[0], f32(w_post, "w_post"), f32(w_pre, "w_pre"), f32(rstd, "rstd", (T, 2)),
-        gh[0], gx[0], oh[0], gy[0], gg[0], f32(dw_post, "dw_post"), f32(dw_pre, "dw_pre"), wp, wn, _stream(stream))
-    _check(st, "poet_block_norm_bwd")
+        ctypes.byref(N), hp[0], yp[0], gp[0], _vec(w_post, "w_post", (d,), f32, dev), _vec(w_pre, "w_pre", (d,), f32, dev),
+        _vec(rstd, "rstd", (T, 2), f32, dev), gh[0], gx[0], oh[0], gy[0], gg[0], _vec(dw_post, "dw_post", (d,), f32, dev),
+        _vec(dw_pre, "dw_pre", (d,), f32, dev), wp, wn, _on_stream(stream, dev))
+    if st:
+        _check(st, "poet_block_norm_bwd")
 
 
 def poet_merge(L: poet_layer, W0, W0_shadow, thetaR, thetaP, primR, primP, idxR, idxP, seed: int, linear_id: int,
