@@ -19,11 +19,20 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // ---- 8 columns of a row --------------------------------------------------------------------------------------------
-// WIDE: adjacent columns 8 g .. 8 g + 7 of group g, in 16-byte accesses (every row of every tensor 16-byte aligned; the
-// last group of an odd d element by element). Else: columns g + k NT of thread g, element by element, for any alignment.
-// Columns past d read as 0.
-template <class T, bool WIDE> struct Cols {
-  static constexpr bool kPacked = WIDE && sizeof(T) == 2;
+// How a thread's 8 columns lie:
+//   EXACT   columns 8 g .. 8 g + 7 of thread g, in 16-byte accesses; every thread has its columns (d = 8 NT)
+//   WIDE    the same where d is any multiple of 8: the threads past it hold zeros
+//   SINGLE  columns g + k NT of thread g, element by element, for any d, pitch and alignment
+// No load is conditional (a thread without columns reads others and drops them): the wait for a token's loads would
+// otherwise have to wait for the stores between them too.
+enum { EXACT = 0, WIDE = 1, SINGLE = 2 };
+// The row's address in scalar registers, for the compiler a new one each time: it would keep a 64-bit address a thread
+// and tensor through the loop over the tokens instead, more than there are registers.
+template <class P> __device__ __forceinline__ P row_at(P p) {
+  return reinterpret_cast<P>(keep_s(reinterpret_cast<uint64_t>(p)));
+}
+template <class T, int FORM> struct Cols {
+  static constexpr bool kPacked = FORM != SINGLE && sizeof(T) == 2;
   u32x4 v[kPacked ? 1 : 2];
   __device__ __forceinline__ float get(int k) const {
     if constexpr (kPacked) {
@@ -33,29 +42,23 @@ template <class T, bool WIDE> struct Cols {
       return __uint_as_float(v[k >> 2][k & 3]);
     }
   }
-  __device__ __forceinline__ void zero() {
+  __device__ __forceinline__ void load(const T* row_, int g, int NT, int d) {
+    const T* row = row_at(row_);
+    if constexpr (FORM == SINGLE) {
 #pragma unroll
-    for (auto& x : v) x = u32x4{0, 0, 0, 0};
-  }
-  __device__ __forceinline__ void load(const T* row, int g, int NT, int d) {
-    zero();
-    if constexpr (WIDE) {
-      const int c = 8 * g;
-      if (c + 8 <= d) {
-#pragma unroll
-        for (unsigned i = 0; i < sizeof(v) / 16; ++i) v[i] = reinterpret_cast<const u32x4*>(row + c)[i];
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + k < d) {
-            if constexpr (kPacked) v[0][k >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[c + k]) << (k & 1) * 16;
-            else v[k >> 2][k & 3] = __float_as_uint((float)row[c + k]);
-          }
+      for (int k = 0; k < 8; ++k) {
+        const int c = g + k * NT;
+        const float f = (float)row[min(c, d - 1)];
+        v[k >> 2][k & 3] = c < d ? __float_as_uint(f) : 0u;
       }
     } else {
+      const bool in = FORM == EXACT || 8 * g < d;
+      const char* p = reinterpret_cast<const char*>(row) + (uint32_t)(in ? g : 0) * (uint32_t)(8 * sizeof(T));
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (g + k * NT < d) v[k >> 2][k & 3] = __float_as_uint((float)row[g + k * NT]);
+      for (unsigned i = 0; i < sizeof(v) / 16; ++i) {
+        v[i] = reinterpret_cast<const u32x4*>(p)[i];
+        if (FORM == WIDE && !in) v[i] = u32x4{0, 0, 0, 0};
+      }
     }
   }
 };
@@ -67,25 +70,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {  // one rounding t
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, b2));
 }
 
-template <class T, bool WIDE> __device__ __forceinline__ void store8(T* row, int g, int NT, int d, const float* f) {
-  if constexpr (WIDE) {
-    const int c = 8 * g;
-    if (c + 8 <= d) {
-      if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<u32x4*>(row + c) = u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
-      } else {
-        reinterpret_cast<float4*>(row + c)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(row + c)[1] = make_float4(f[4], f[5], f[6], f[7]);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k < d) row[c + k] = (T)f[k];
-    }
-  } else {
+template <class T, int FORM> __device__ __forceinline__ void store8(T* row_, int g, int NT, int d, const float* f) {
+  T* row = row_at(row_);
+  if constexpr (FORM == SINGLE) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (g + k * NT < d) row[g + k * NT] = (T)f[k];
+  } else if (FORM == EXACT || 8 * g < d) {
+    char* p = reinterpret_cast<char*>(row) + (uint32_t)g * (uint32_t)(8 * sizeof(T));
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<u32x4*>(p) = u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+    } else {
+      reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
   }
 }
 
@@ -117,44 +115,52 @@ __device__ __forceinline__ float block_sum(float v, float (*red)[16], int& turn)
   return s;
 }
 
+// Which parts a call has, known to the compiler for the common ones (y, x and their gradients, and h' from past the seam,
+// all given); PARTS_ANY looks at the arguments.
+enum { PARTS_POST = 1, PARTS_GATE = 2, PARTS_ANY = 4 };
+
 // ---- forward --------------------------------------------------------------------------------------------------------
-template <class TR, class TA, int VPT, bool WIDE>
-__global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs a) {
+template <class TR, class TA, int MAXT, int VPT, int FORM, int PARTS>
+__global__ __launch_bounds__(MAXT) void k_norm_fwd(const NormArgs a) {
   __shared__ float red[2][16];
+  constexpr bool kAny = PARTS == PARTS_ANY;
+  const bool post = kAny ? a.w_post != nullptr : (PARTS & PARTS_POST) != 0;
+  const bool gate = kAny ? a.gate != nullptr : (PARTS & PARTS_GATE) != 0;
+  const bool has_y = kAny ? a.y != nullptr : true, has_x = kAny ? a.x != nullptr : true;
   const int tid = threadIdx.x, NT = blockDim.x, d = a.d;
+  const auto col = [&](int i) { return FORM == SINGLE ? tid + i * 8 * NT : tid + i * NT; };
   int turn = 0;
   const float inv_d = 1.f / (float)d;
-  Cols<float, WIDE> wq[VPT], wp[VPT];
-  Cols<TR, WIDE> h[VPT];
-  Cols<TA, WIDE> y[VPT], g[VPT];
+  Cols<float, FORM> wq[VPT], wp[VPT];
+  Cols<TR, FORM> h[VPT];
+  Cols<TA, FORM> y[VPT], g[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = WIDE ? tid + i * NT : tid + i * 8 * NT;
-    if (a.w_post) wq[i].load(a.w_post, c, NT, d);
-    if (a.w_pre) wp[i].load(a.w_pre, c, NT, d);
+    if (post) wq[i].load(a.w_post, col(i), NT, d);
+    if (has_x) wp[i].load(a.w_pre, col(i), NT, d);
   }
   const auto fetch = [&](int64_t t) {
+    const int64_t gr = a.gate_tokens == 1 ? t : (int64_t)((uint32_t)t / (uint32_t)max(a.gate_tokens, 1));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = WIDE ? tid + i * NT : tid + i * 8 * NT;
-      h[i].load((const TR*)a.h + t * a.ldh, c, NT, d);
-      if (a.y) y[i].load((const TA*)a.y + t * a.ldy, c, NT, d);
-      if (a.gate) g[i].load((const TA*)a.gate + (a.gate_tokens == 1 ? t : t / a.gate_tokens) * a.ldg, c, NT, d);
+      h[i].load((const TR*)a.h + t * a.ldh, col(i), NT, d);
+      if (has_y) y[i].load((const TA*)a.y + t * a.ldy, col(i), NT, d);
+      if (gate) g[i].load((const TA*)a.gate + gr * a.ldg, col(i), NT, d);
     }
   };
-  if (VPT == 1) fetch(blockIdx.x);  // two groups a thread leave no registers for the next token's columns
+  if (MAXT <= 512) fetch(blockIdx.x);  // 1024 threads of two groups have no registers for the next token's columns
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    if (VPT > 1) fetch(t);
+    if (MAXT > 512) fetch(t);
     float f[VPT][8], r[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         f[i][k] = h[i].get(k);
-        r[i][k] = a.y ? y[i].get(k) : 0.f;
+        r[i][k] = has_y ? y[i].get(k) : 0.f;
       }
     float ry = 1.f, s = 0.f;
-    if (a.w_post) {
+    if (post) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -166,28 +172,27 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs a) {
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (a.y) {
+        if (has_y) {
           float b = r[i][k];
-          if (a.w_post) b = b * ry * wq[i].get(k);
-          if (a.gate) b *= g[i].get(k);
+          if (post) b = b * ry * wq[i].get(k);
+          if (gate) b *= g[i].get(k);
           f[i][k] = rounded<TR>(fmaf(f[i][k], a.res_scale, b));  // the norm reads the residual stream as it is kept
         }
         s = fmaf(f[i][k], f[i][k], s);
       }
-    if (VPT == 1 && t + gridDim.x < a.T) fetch(t + gridDim.x);
-    if (a.h_out) {
+    if (MAXT <= 512) fetch(t + gridDim.x < a.T ? t + gridDim.x : t);
+    if (has_y) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        store8<TR, WIDE>((TR*)a.h_out + t * a.ldh, WIDE ? tid + i * NT : tid + i * 8 * NT, NT, d, f[i]);
+      for (int i = 0; i < VPT; ++i) store8<TR, FORM>((TR*)a.h_out + t * a.ldh, col(i), NT, d, f[i]);
     }
     float rh = 0.f;
-    if (a.x) {
+    if (has_x) {
       rh = 1.f / sqrtf(block_sum(s, red, turn) * inv_d + a.eps);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[i][k] = f[i][k] * rh * wp[i].get(k);
-        store8<TA, WIDE>((TA*)a.x + t * a.ldx, WIDE ? tid + i * NT : tid + i * 8 * NT, NT, d, f[i]);
+        store8<TA, FORM>((TA*)a.x + t * a.ldx, col(i), NT, d, f[i]);
       }
     }
     if (tid == 0) { a.rstd[2 * t] = ry; a.rstd[2 * t + 1] = rh; }
@@ -216,46 +221,70 @@ __host__ __device__ inline void chunk_range(const NormPlan& p, int T, int c, int
   if (t1 > T) t1 = T;
 }
 
-template <class TR, class TA, int VPT, bool WIDE>
-__global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs a, const NormPlan p, float* part) {
+template <class TR, class TA, int MAXT, int VPT, int FORM, int PARTS>
+__global__ __launch_bounds__(MAXT, MAXT <= 512 ? 3 : 4) void k_norm_bwd(const NormArgs a, const NormPlan p, float* part) {
   __shared__ float red[2][16];
+  constexpr bool kAny = PARTS == PARTS_ANY;
+  const bool post = kAny ? a.w_post != nullptr : (PARTS & PARTS_POST) != 0;
+  const bool gate = kAny ? a.gate != nullptr : (PARTS & PARTS_GATE) != 0;
+  const bool has_dx = kAny ? a.dx != nullptr : true, has_dh = kAny ? a.dh_out != nullptr : true;
+  const bool has_dy = kAny ? a.dy != nullptr : true, has_y = post || gate;  // dy alone needs no y
   const int tid = threadIdx.x, NT = blockDim.x, d = a.d;
+  const auto col = [&](int i) { return FORM == SINGLE ? tid + i * 8 * NT : tid + i * NT; };
   int turn = 0;
   const float inv_d = 1.f / (float)d;
   int64_t t0, t1;
   chunk_range(p, a.T, blockIdx.x, t0, t1);
-  Cols<float, WIDE> wq[VPT], wp[VPT];
-  Cols<TR, WIDE> h[VPT], e[VPT];
-  Cols<TA, WIDE> y[VPT], g[VPT], x[VPT];
+  Cols<float, FORM> wq[VPT], wp[VPT];
+  Cols<TR, FORM> h[VPT], e[VPT];
+  Cols<TA, FORM> y[VPT], g[VPT], x[VPT];
   float spre[VPT][8], spost[VPT][8], sg[VPT][8];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = WIDE ? tid + i * NT : tid + i * 8 * NT;
-    if (a.w_post) wq[i].load(a.w_post, c, NT, d);
-    if (a.w_pre) wp[i].load(a.w_pre, c, NT, d);
+    if (post) wq[i].load(a.w_post, col(i), NT, d);
+    if (has_dx) wp[i].load(a.w_pre, col(i), NT, d);
 #pragma unroll
     for (int k = 0; k < 8; ++k) spre[i][k] = spost[i][k] = sg[i][k] = 0.f;
   }
+  // a token's columns, each tensor's as soon as the token before has used its own
   float ry = 1.f, rh = 0.f;
-  const auto fetch = [&](int64_t t) {
+  int zero = 0;
+  asm volatile("" : "+v"(zero));  // the two factors through vector memory: a scalar load would share the sums' wait
+  int64_t gr = gate ? (a.gate_tokens == 1 ? t0 : (int64_t)((uint32_t)t0 / (uint32_t)a.gate_tokens)) : 0;
+  int left = gate ? (int)min((gr + 1) * a.gate_tokens, t1) - (int)t0 : 0;  // tokens of this gate row and chunk still to come
+  const auto fetch_x = [&](int64_t t) {
+    if (post) ry = a.rstd[2 * t + zero];
+    if (!has_dx) return;
+    rh = a.rstd[2 * t + 1 + zero];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = WIDE ? tid + i * NT : tid + i * 8 * NT;
-      if (a.dx) { h[i].load((const TR*)a.h + t * a.ldh, c, NT, d); x[i].load((const TA*)a.dx + t * a.ldx, c, NT, d); }
-      if (a.dh_out) e[i].load((const TR*)a.dh_out + t * a.ldh, c, NT, d);
-      if (a.y) y[i].load((const TA*)a.y + t * a.ldy, c, NT, d);
-      if (a.gate) g[i].load((const TA*)a.gate + (a.gate_tokens == 1 ? t : t / a.gate_tokens) * a.ldg, c, NT, d);
+      h[i].load((const TR*)a.h + t * a.ldh, col(i), NT, d);
+      x[i].load((const TA*)a.dx + t * a.ldx, col(i), NT, d);
     }
-    ry = a.w_post ? a.rstd[2 * t] : 1.f;
-    rh = a.rstd[2 * t + 1];
   };
-  if (VPT == 1 && t0 < t1) fetch(t0);
+  const auto fetch_e = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (has_dh) e[i].load((const TR*)a.dh_out + t * a.ldh, col(i), NT, d);
+  };
+  const auto fetch_y = [&](int64_t t, int64_t row) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (has_y) y[i].load((const TA*)a.y + t * a.ldy, col(i), NT, d);
+      if (gate) g[i].load((const TA*)a.gate + row * a.ldg, col(i), NT, d);
+    }
+  };
+  if (t0 < t1) {
+    fetch_x(t0);
+    fetch_e(t0);
+    fetch_y(t0, gr);
+  }
   for (int64_t t = t0; t < t1; ++t) {
-    if (VPT > 1) fetch(t);
+    const int64_t tn = t + 1 < t1 ? t + 1 : t;  // the last token is fetched again rather than not
     float f[VPT][8], b[VPT][8], v[VPT][8];
     const float ryt = ry, rht = rh;
     float s = 0.f;
-    if (a.dx) {
+    if (has_dx) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -266,41 +295,52 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs a, const NormP
           spre[i][k] = fmaf(dx, n, spre[i][k]);
           s = fmaf(f[i][k], n, s);
         }
+      fetch_x(tn);
       const float c1 = block_sum(s, red, turn) * inv_d;
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[i][k] = rht * fmaf(-v[i][k], c1, f[i][k]) + (a.dh_out ? e[i].get(k) : 0.f);
+        for (int k = 0; k < 8; ++k) f[i][k] = rht * fmaf(-v[i][k], c1, f[i][k]) + (has_dh ? e[i].get(k) : 0.f);
     } else {
+      fetch_x(tn);
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[i][k] = e[i].get(k);
     }
+    fetch_e(tn);
     // f: the gradient of h'. Of the block's output: v before its norm's mean, b the normalized output.
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        b[i][k] = a.y ? y[i].get(k) * ryt : 0.f;
-        const float tg = a.gate ? f[i][k] * g[i].get(k) : f[i][k];
-        v[i][k] = a.w_post ? tg * wq[i].get(k) : tg;
-        spost[i][k] = fmaf(tg, b[i][k], spost[i][k]);
-        if (a.gate) sg[i][k] = fmaf(a.w_post ? f[i][k] * wq[i].get(k) : f[i][k], b[i][k], sg[i][k]);
-        s = fmaf(v[i][k], b[i][k], s);
+        const float tg = gate ? f[i][k] * g[i].get(k) : f[i][k];
+        v[i][k] = post ? tg * wq[i].get(k) : tg;
+        if (!has_y) continue;
+        b[i][k] = post ? y[i].get(k) * ryt : y[i].get(k);
+        if (post) {
+          spost[i][k] = fmaf(tg, b[i][k], spost[i][k]);
+          s = fmaf(v[i][k], b[i][k], s);
+        }
+        if (gate) sg[i][k] = fmaf(post ? f[i][k] * wq[i].get(k) : f[i][k], b[i][k], sg[i][k]);
       }
-    if (VPT == 1 && t + 1 < t1) fetch(t + 1);
-    if (a.gate && p.split == 1 && (a.gate_tokens == 1 || t + 1 == t1 || (t + 1) % a.gate_tokens == 0)) {
-      const int64_t gr = a.gate_tokens == 1 ? t : t / a.gate_tokens;
+    const int64_t row = gr;
+    const bool flush = gate && --left == 0;
+    if (flush) {
+      ++gr;
+      left = (int)min((int64_t)a.gate_tokens, t1 - (t + 1));
+    }
+    fetch_y(tn, t + 1 < t1 ? gr : row);
+    if (flush && p.split == 1) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        store8<TA, WIDE>((TA*)a.dgate + gr * a.ldg, WIDE ? tid + i * NT : tid + i * 8 * NT, NT, d, sg[i]);
+        store8<TA, FORM>((TA*)a.dgate + row * a.ldg, col(i), NT, d, sg[i]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) sg[i][k] = 0.f;
       }
     }
-    if (a.w_post) {
+    if (post) {
       const float c2 = block_sum(s, red, turn) * inv_d;
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
@@ -309,25 +349,20 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs a, const NormP
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = WIDE ? tid + i * NT : tid + i * 8 * NT;
-      if (a.dy) store8<TA, WIDE>((TA*)a.dy + t * a.ldy, c, NT, d, v[i]);
+      if (has_dy) store8<TA, FORM>((TA*)a.dy + t * a.ldy, col(i), NT, d, v[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[i][k] *= a.res_scale;
-      store8<TR, WIDE>((TR*)a.dh + t * a.ldh, c, NT, d, f[i]);
+      store8<TR, FORM>((TR*)a.dh + t * a.ldh, col(i), NT, d, f[i]);
     }
   }
   // this chunk's sums: [chunk][pre, post, gate row][d]
   float* q = part + (int64_t)blockIdx.x * 3 * d;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = WIDE ? 8 * (tid + i * NT) + k : tid + (i * 8 + k) * NT;
-      if (c >= d) continue;
-      if (a.dw_pre) q[c] = spre[i][k];
-      if (a.dw_post) q[d + c] = spost[i][k];
-      if (p.split > 1) q[2 * (int64_t)d + c] = sg[i][k];
-    }
+  for (int i = 0; i < VPT; ++i) {
+    if (has_dx) store8<float, FORM>(q, col(i), NT, d, spre[i]);
+    if (post) store8<float, FORM>(q + d, col(i), NT, d, spost[i]);
+    if (gate && p.split > 1) store8<float, FORM>(q + 2 * (int64_t)d, col(i), NT, d, sg[i]);
+  }
 }
 
 // Adds the chunks' sums: y = 0, 1: all chunks into dw_pre, dw_post; y = 2 + r: the chunks of gate row r (stored as TA).
@@ -360,20 +395,23 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const NormArgs a, const Norm
 }
 
 // ---- launches -------------------------------------------------------------------------------------------------------
-int threads_of(int d) { return d <= 8192 ? (d + 511) / 512 * 64 : 1024; }
+// 8 columns a thread up to 512 threads, 16 beyond
+int threads_of(int d) { return d <= 4096 ? (d + 511) / 512 * 64 : (d + 1023) / 1024 * 64; }
 
 NormPlan plan_of(int T, int d, int gate_tokens) {
-  // about 16 waves a CU (256 CUs) in one round of workgroups, but at most 256 tokens in a row of float32 additions
-  const int groups = std::max(1, 4096 / (threads_of(d) / 64));
-  const int len = std::min(256, std::max(1, (T + groups - 1) / groups));
+  // workgroups of about 10 waves a CU (256 CUs) in one round, a few tokens each at least (the sums of a chunk are as many
+  // bytes as 3 to 6 of a token's rows), but at most 256 tokens in a row of float32 additions
+  const int groups = 256 * std::max(1, 10 / (threads_of(d) / 64));
+  const int len = std::min(256, std::max(std::min(T, 2), (T + groups - 1) / groups));
   NormPlan p;
   p.len = len;
   const int run = std::min(gate_tokens, T);
   if (run > len) {
-    p.split = (run + len - 1) / len;
+    const int runs = (T + run - 1) / run;
+    p.split = std::min((run + len - 1) / len, std::max({1, groups / runs, (run + 255) / 256}));
     p.len = (run + p.split - 1) / p.split;
     p.run = run;
-    p.chunks = (T + run - 1) / run * p.split;
+    p.chunks = runs * p.split;
   } else {
     if (run > 1) p.len = len / run * run;
     p.chunks = (T + p.len - 1) / p.len;
@@ -383,26 +421,43 @@ NormPlan plan_of(int T, int d, int gate_tokens) {
 
 bool al16(const void* p, int64_t ld, size_t e) { return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * (int64_t)e % 16 == 0); }
 
-bool wide_of(const NormArgs& a) {
+int form_of(const NormArgs& a) {
   const size_t r = dtype_size(a.res_dt), v = dtype_size(a.act_dt);
-  return al16(a.h, a.ldh, r) && al16(a.h_out, a.ldh, r) && al16(a.dh_out, a.ldh, r) && al16(a.dh, a.ldh, r) &&
-         al16(a.y, a.ldy, v) && al16(a.dy, a.ldy, v) && al16(a.gate, a.ldg, v) && al16(a.dgate, a.ldg, v) &&
-         al16(a.x, a.ldx, v) && al16(a.dx, a.ldx, v) && al16(a.w_post, 0, 4) && al16(a.w_pre, 0, 4);
+  const bool wide = a.d % 8 == 0 &&
+      al16(a.h, a.ldh, r) && al16(a.h_out, a.ldh, r) && al16(a.dh_out, a.ldh, r) && al16(a.dh, a.ldh, r) &&
+      al16(a.y, a.ldy, v) && al16(a.dy, a.ldy, v) && al16(a.gate, a.ldg, v) && al16(a.dgate, a.ldg, v) &&
+      al16(a.x, a.ldx, v) && al16(a.dx, a.ldx, v) && al16(a.w_post, 0, 4) && al16(a.w_pre, 0, 4);
+  return !wide ? SINGLE : a.d == 8 * threads_of(a.d) ? EXACT : WIDE;
 }
 
-template <int V, bool W> struct Form { static constexpr int VPT = V; static constexpr bool WIDE = W; };
-template <class F> hipError_t by_form(const NormArgs& a, F f) {
-  const auto types = [&](auto form) {
-    if (a.res_dt == BF16) {
-      if (a.act_dt == BF16) f(__bf16(), __bf16(), form); else f(__bf16(), float(), form);
-    } else {
-      if (a.act_dt == BF16) f(float(), __bf16(), form); else f(float(), float(), form);
-    }
-  };
-  if (a.d <= 8192) {
-    if (wide_of(a)) types(Form<1, true>()); else types(Form<1, false>());
+template <int M, int V, int F, int P> struct Form { static constexpr int MAXT = M, VPT = V, FORM = F, PARTS = P; };
+template <class F> void by_types(const NormArgs& a, F f) {
+  if (a.res_dt == BF16) {
+    if (a.act_dt == BF16) f(__bf16(), __bf16()); else f(__bf16(), float());
   } else {
-    if (wide_of(a)) types(Form<2, true>()); else types(Form<2, false>());
+    if (a.act_dt == BF16) f(float(), __bf16()); else f(float(), float());
+  }
+}
+template <int FORM, class F> void by_parts(const NormArgs& a, bool all, F f) {
+  if (!all) f(Form<512, 1, FORM, PARTS_ANY>());
+  else if (a.w_post && a.gate) f(Form<512, 1, FORM, PARTS_POST | PARTS_GATE>());
+  else if (a.w_post) f(Form<512, 1, FORM, PARTS_POST>());
+  else if (a.gate) f(Form<512, 1, FORM, PARTS_GATE>());
+  else f(Form<512, 1, FORM, 0>());
+}
+// all: every part but post norm and gate is given
+template <class F> hipError_t by_form(const NormArgs& a, bool all, F f) {
+  const int form = form_of(a);
+  if (a.d > 8192) {
+    if (form == SINGLE) f(Form<1024, 2, SINGLE, PARTS_ANY>()); else f(Form<1024, 2, WIDE, PARTS_ANY>());
+  } else if (a.d > 4096) {
+    if (form == SINGLE) f(Form<512, 2, SINGLE, PARTS_ANY>()); else f(Form<512, 2, WIDE, PARTS_ANY>());
+  } else if (form == EXACT) {
+    by_parts<EXACT>(a, all, f);
+  } else if (form == WIDE) {
+    by_parts<WIDE>(a, all, f);
+  } else {
+    by_parts<SINGLE>(a, all, f);
   }
   return hipGetLastError();
 }
@@ -421,9 +476,11 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st) {
   ProfScope prof(POET_K_NORM, st, 10.0 * a.T * a.d, moved(a, a.y ? 2 : 1, (a.y ? 1 : 0) + (a.x ? 1 : 0)));
   const int nt = threads_of(a.d);
   const int grid = std::min(a.T, 256 * std::max(1, 2048 / nt));
-  return by_form(a, [&](auto r, auto v, auto form) {
+  return by_form(a, a.y && a.x, [&](auto form) {
     using F = decltype(form);
-    hipLaunchKernelGGL((k_norm_fwd<decltype(r), decltype(v), F::VPT, F::WIDE>), dim3(grid), dim3(nt), 0, st, a);
+    by_types(a, [&](auto r, auto v) {
+      hipLaunchKernelGGL((k_norm_fwd<decltype(r), decltype(v), F::MAXT, F::VPT, F::FORM, F::PARTS>), dim3(grid), dim3(nt), 0, st, a);
+    });
   });
 }
 
@@ -433,10 +490,12 @@ hipError_t launch_norm_bwd(const NormArgs& a, void* ws, hipStream_t st) {
   {
     ProfScope prof(POET_K_NORM, st, 25.0 * a.T * a.d,
                    moved(a, 1 + (a.dx ? 1 : 0) + (a.dh_out ? 1 : 0), (a.dx ? 1 : 0) + (a.y ? 1 : 0) + (a.dy ? 1 : 0)));
-    const hipError_t e = by_form(a, [&](auto r, auto v, auto form) {
+    const hipError_t e = by_form(a, a.dx && a.dh_out && a.dy, [&](auto form) {
       using F = decltype(form);
-      hipLaunchKernelGGL((k_norm_bwd<decltype(r), decltype(v), F::VPT, F::WIDE>), dim3(p.chunks), dim3(threads_of(a.d)), 0,
-                         st, a, p, part);
+      by_types(a, [&](auto r, auto v) {
+        hipLaunchKernelGGL((k_norm_bwd<decltype(r), decltype(v), F::MAXT, F::VPT, F::FORM, F::PARTS>), dim3(p.chunks),
+                           dim3(threads_of(a.d)), 0, st, a, p, part);
+      });
     });
     if (e != hipSuccess) return e;
   }
