@@ -20,19 +20,32 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // ---- 8 columns of a row --------------------------------------------------------------------------------------------
 // How a thread's 8 columns lie:
-//   EXACT   columns 8 g .. 8 g + 7 of thread g, in 16-byte accesses; every thread has its columns (d = 8 NT)
-//   WIDE    the same where d is any multiple of 8: the threads past it hold zeros
-//   SINGLE  columns g + k NT of thread g, element by element, for any d, pitch and alignment
-// No load is conditional (a thread without columns reads others and drops them): the wait for a token's loads would
-// otherwise have to wait for the stores between them too.
+//   EXACT   columns 8 g .. 8 g + 7 of thread g; every thread has its columns (d = 8 NT)
+//   WIDE    the same for any d >= 8: where d is no multiple of 8 the last thread with columns reads the row's last 8 and
+//           drops those that are its neighbour's; threads past it read them too and drop all
+//   SINGLE  column g of thread g (d < 8, one element a thread)
+// EXACT and WIDE read and write 16 bytes at a time whatever the row's alignment (global accesses need none). No load is
+// conditional: the wait for a token's loads would otherwise have to wait for the stores between them too.
 enum { EXACT = 0, WIDE = 1, SINGLE = 2 };
 // The row's address in scalar registers, for the compiler a new one each time: it would keep a 64-bit address a thread
 // and tensor through the loop over the tokens instead, more than there are registers.
-template <class P> __device__ __forceinline__ P row_at(P p) {
-  return reinterpret_cast<P>(keep_s(reinterpret_cast<uint64_t>(p)));
+typedef __attribute__((address_space(1))) char GlobalByte;  // global memory, or the accesses would count as LDS's too
+typedef u32x4 u32x4_any __attribute__((aligned(2)));        // 16 bytes at an element's alignment
+typedef __attribute__((address_space(1))) u32x4_any Global16;
+template <class T> __device__ __forceinline__ GlobalByte* row_at(const T* p) {
+  return reinterpret_cast<GlobalByte*>(keep_s(reinterpret_cast<uint64_t>(p)));
 }
+// thread g's place in rows of d columns: the first column it reads, and how many of the 8 are not its own
+struct Place {
+  int c, skip;
+  template <int FORM> static __device__ __forceinline__ Place of(int g, int d) {
+    if (FORM == EXACT) return {8 * g, 0};
+    if (FORM == SINGLE) return {g < d ? g : 0, g < d ? 0 : 8};
+    return {min(8 * g, d - 8), max(0, min(8, 8 * g - (d - 8)))};
+  }
+};
 template <class T, int FORM> struct Cols {
-  static constexpr bool kPacked = FORM != SINGLE && sizeof(T) == 2;
+  static constexpr bool kPacked = sizeof(T) == 2;
   u32x4 v[kPacked ? 1 : 2];
   __device__ __forceinline__ float get(int k) const {
     if constexpr (kPacked) {
@@ -42,23 +55,25 @@ template <class T, int FORM> struct Cols {
       return __uint_as_float(v[k >> 2][k & 3]);
     }
   }
-  __device__ __forceinline__ void load(const T* row_, int g, int NT, int d) {
-    const T* row = row_at(row_);
+  __device__ __forceinline__ void load(const T* row, Place p) {
     if constexpr (FORM == SINGLE) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int c = g + k * NT;
-        const float f = (float)row[min(c, d - 1)];
-        v[k >> 2][k & 3] = c < d ? __float_as_uint(f) : 0u;
-      }
+      for (auto& x : v) x = u32x4{0, 0, 0, 0};
+      if constexpr (kPacked) v[0][0] = __builtin_bit_cast(uint16_t, row[p.c]);
+      else v[0][0] = __float_as_uint(row[p.c]);
     } else {
-      const bool in = FORM == EXACT || 8 * g < d;
-      const char* p = reinterpret_cast<const char*>(row) + (uint32_t)(in ? g : 0) * (uint32_t)(8 * sizeof(T));
+      const GlobalByte* at = row_at(row) + (uint32_t)p.c * (uint32_t)sizeof(T);
 #pragma unroll
-      for (unsigned i = 0; i < sizeof(v) / 16; ++i) {
-        v[i] = reinterpret_cast<const u32x4*>(p)[i];
-        if (FORM == WIDE && !in) v[i] = u32x4{0, 0, 0, 0};
-      }
+      for (unsigned i = 0; i < sizeof(v) / 16; ++i) v[i] = reinterpret_cast<const Global16*>(at)[i];
+    }
+  }
+  // once the columns have arrived: 0 for those that are not this thread's
+  __device__ __forceinline__ void own(Place p) {
+    if (FORM == EXACT || p.skip == 0) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k >= p.skip) continue;
+      if constexpr (kPacked) v[0][k >> 1] &= k & 1 ? 0xffffu : 0xffff0000u;
+      else v[k >> 2][k & 3] = 0u;
     }
   }
 };
@@ -70,19 +85,24 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {  // one rounding t
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, b2));
 }
 
-template <class T, int FORM> __device__ __forceinline__ void store8(T* row_, int g, int NT, int d, const float* f) {
-  T* row = row_at(row_);
+template <class T, int FORM> __device__ __forceinline__ void store8(T* row, Place p, const float* f) {
   if constexpr (FORM == SINGLE) {
+    if (p.skip == 0) row[p.c] = (T)f[0];
+  } else {
+    GlobalByte* at = row_at(row) + (uint32_t)p.c * (uint32_t)sizeof(T);
+    if (FORM == EXACT || p.skip == 0) {
+      if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<Global16*>(at) = u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+      } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (g + k * NT < d) row[g + k * NT] = (T)f[k];
-  } else if (FORM == EXACT || 8 * g < d) {
-    char* p = reinterpret_cast<char*>(row) + (uint32_t)g * (uint32_t)(8 * sizeof(T));
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<u32x4*>(p) = u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+        for (int i = 0; i < 2; ++i)
+          reinterpret_cast<Global16*>(at)[i] = u32x4{__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                                                     __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3])};
+      }
     } else {
-      reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+      for (int k = 1; k < 8; ++k)
+        if (k >= p.skip) row[p.c + k] = (T)f[k];
     }
   }
 }
@@ -128,7 +148,9 @@ __global__ __launch_bounds__(MAXT) void k_norm_fwd(const NormArgs a) {
   const bool gate = kAny ? a.gate != nullptr : (PARTS & PARTS_GATE) != 0;
   const bool has_y = kAny ? a.y != nullptr : true, has_x = kAny ? a.x != nullptr : true;
   const int tid = threadIdx.x, NT = blockDim.x, d = a.d;
-  const auto col = [&](int i) { return FORM == SINGLE ? tid + i * 8 * NT : tid + i * NT; };
+  Place at[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) at[i] = Place::of<FORM>(tid + i * NT, d);
   int turn = 0;
   const float inv_d = 1.f / (float)d;
   Cols<float, FORM> wq[VPT], wp[VPT];
@@ -136,29 +158,32 @@ __global__ __launch_bounds__(MAXT) void k_norm_fwd(const NormArgs a) {
   Cols<TA, FORM> y[VPT], g[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    if (post) wq[i].load(a.w_post, col(i), NT, d);
-    if (has_x) wp[i].load(a.w_pre, col(i), NT, d);
+    if (post) wq[i].load(a.w_post, at[i]);  // a column's weight is only met by its value: no own()
+    if (has_x) wp[i].load(a.w_pre, at[i]);
   }
   const auto fetch = [&](int64_t t) {
     const int64_t gr = a.gate_tokens == 1 ? t : (int64_t)((uint32_t)t / (uint32_t)max(a.gate_tokens, 1));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      h[i].load((const TR*)a.h + t * a.ldh, col(i), NT, d);
-      if (has_y) y[i].load((const TA*)a.y + t * a.ldy, col(i), NT, d);
-      if (gate) g[i].load((const TA*)a.gate + gr * a.ldg, col(i), NT, d);
+      h[i].load((const TR*)a.h + t * a.ldh, at[i]);
+      if (has_y) y[i].load((const TA*)a.y + t * a.ldy, at[i]);
+      if (gate) g[i].load((const TA*)a.gate + gr * a.ldg, at[i]);
     }
   };
-  if (MAXT <= 512) fetch(blockIdx.x);  // 1024 threads of two groups have no registers for the next token's columns
+  if (VPT == 1) fetch(blockIdx.x);  // 1024 threads of two groups have no registers for the next token's columns
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    if (MAXT > 512) fetch(t);
+    if (VPT > 1) fetch(t);
     float f[VPT][8], r[VPT][8];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < VPT; ++i) {
+      h[i].own(at[i]);
+      if (has_y) y[i].own(at[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         f[i][k] = h[i].get(k);
         r[i][k] = has_y ? y[i].get(k) : 0.f;
       }
+    }
     float ry = 1.f, s = 0.f;
     if (post) {
 #pragma unroll
@@ -180,10 +205,10 @@ __global__ __launch_bounds__(MAXT) void k_norm_fwd(const NormArgs a) {
         }
         s = fmaf(f[i][k], f[i][k], s);
       }
-    if (MAXT <= 512) fetch(t + gridDim.x < a.T ? t + gridDim.x : t);
+    if (VPT == 1) fetch(t + gridDim.x < a.T ? t + gridDim.x : t);
     if (has_y) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) store8<TR, FORM>((TR*)a.h_out + t * a.ldh, col(i), NT, d, f[i]);
+      for (int i = 0; i < VPT; ++i) store8<TR, FORM>((TR*)a.h_out + t * a.ldh, at[i], f[i]);
     }
     float rh = 0.f;
     if (has_x) {
@@ -192,7 +217,7 @@ __global__ __launch_bounds__(MAXT) void k_norm_fwd(const NormArgs a) {
       for (int i = 0; i < VPT; ++i) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[i][k] = f[i][k] * rh * wp[i].get(k);
-        store8<TA, FORM>((TA*)a.x + t * a.ldx, col(i), NT, d, f[i]);
+        store8<TA, FORM>((TA*)a.x + t * a.ldx, at[i], f[i]);
       }
     }
     if (tid == 0) { a.rstd[2 * t] = ry; a.rstd[2 * t + 1] = rh; }
@@ -230,7 +255,9 @@ __global__ __launch_bounds__(MAXT, MAXT <= 512 ? 3 : 4) void k_norm_bwd(const No
   const bool has_dx = kAny ? a.dx != nullptr : true, has_dh = kAny ? a.dh_out != nullptr : true;
   const bool has_dy = kAny ? a.dy != nullptr : true, has_y = post || gate;  // dy alone needs no y
   const int tid = threadIdx.x, NT = blockDim.x, d = a.d;
-  const auto col = [&](int i) { return FORM == SINGLE ? tid + i * 8 * NT : tid + i * NT; };
+  Place at[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) at[i] = Place::of<FORM>(tid + i * NT, d);
   int turn = 0;
   const float inv_d = 1.f / (float)d;
   int64_t t0, t1;
@@ -241,8 +268,8 @@ __global__ __launch_bounds__(MAXT, MAXT <= 512 ? 3 : 4) void k_norm_bwd(const No
   float spre[VPT][8], spost[VPT][8], sg[VPT][8];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    if (post) wq[i].load(a.w_post, col(i), NT, d);
-    if (has_dx) wp[i].load(a.w_pre, col(i), NT, d);
+    if (post) wq[i].load(a.w_post, at[i]);
+    if (has_dx) wp[i].load(a.w_pre, at[i]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) spre[i][k] = spost[i][k] = sg[i][k] = 0.f;
   }
@@ -258,20 +285,20 @@ __global__ __launch_bounds__(MAXT, MAXT <= 512 ? 3 : 4) void k_norm_bwd(const No
     rh = a.rstd[2 * t + 1 + zero];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      h[i].load((const TR*)a.h + t * a.ldh, col(i), NT, d);
-      x[i].load((const TA*)a.dx + t * a.ldx, col(i), NT, d);
+      h[i].load((const TR*)a.h + t * a.ldh, at[i]);
+      x[i].load((const TA*)a.dx + t * a.ldx, at[i]);
     }
   };
   const auto fetch_e = [&](int64_t t) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      if (has_dh) e[i].load((const TR*)a.dh_out + t * a.ldh, col(i), NT, d);
+      if (has_dh) e[i].load((const TR*)a.dh_out + t * a.ldh, at[i]);
   };
   const auto fetch_y = [&](int64_t t, int64_t row) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      if (has_y) y[i].load((const TA*)a.y + t * a.ldy, col(i), NT, d);
-      if (gate) g[i].load((const TA*)a.gate + row * a.ldg, col(i), NT, d);
+      if (has_y) y[i].load((const TA*)a.y + t * a.ldy, at[i]);
+      if (gate) g[i].load((const TA*)a.gate + row * a.ldg, at[i]);
     }
   };
   if (t0 < t1) {
@@ -285,6 +312,11 @@ __global__ __launch_bounds__(MAXT, MAXT <= 512 ? 3 : 4) void k_norm_bwd(const No
     const float ryt = ry, rht = rh;
     float s = 0.f;
     if (has_dx) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        h[i].own(at[i]);
+        x[i].own(at[i]);
+      }
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -311,6 +343,10 @@ __global__ __launch_bounds__(MAXT, MAXT <= 512 ? 3 : 4) void k_norm_bwd(const No
     fetch_e(tn);
     // f: the gradient of h'. Of the block's output: v before its norm's mean, b the normalized output.
     s = 0.f;
+    if (has_y) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) y[i].own(at[i]);
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -335,7 +371,7 @@ __global__ __launch_bounds__(MAXT, MAXT <= 512 ? 3 : 4) void k_norm_bwd(const No
     if (flush && p.split == 1) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        store8<TA, FORM>((TA*)a.dgate + row * a.ldg, col(i), NT, d, sg[i]);
+        store8<TA, FORM>((TA*)a.dgate + row * a.ldg, at[i], sg[i]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) sg[i][k] = 0.f;
       }
@@ -349,19 +385,19 @@ __global__ __launch_bounds__(MAXT, MAXT <= 512 ? 3 : 4) void k_norm_bwd(const No
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      if (has_dy) store8<TA, FORM>((TA*)a.dy + t * a.ldy, col(i), NT, d, v[i]);
+      if (has_dy) store8<TA, FORM>((TA*)a.dy + t * a.ldy, at[i], v[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[i][k] *= a.res_scale;
-      store8<TR, FORM>((TR*)a.dh + t * a.ldh, col(i), NT, d, f[i]);
+      store8<TR, FORM>((TR*)a.dh + t * a.ldh, at[i], f[i]);
     }
   }
   // this chunk's sums: [chunk][pre, post, gate row][d]
   float* q = part + (int64_t)blockIdx.x * 3 * d;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    if (has_dx) store8<float, FORM>(q, col(i), NT, d, spre[i]);
-    if (post) store8<float, FORM>(q + d, col(i), NT, d, spost[i]);
-    if (gate && p.split > 1) store8<float, FORM>(q + 2 * (int64_t)d, col(i), NT, d, sg[i]);
+    if (has_dx) store8<float, FORM>(q, at[i], spre[i]);
+    if (post) store8<float, FORM>(q + d, at[i], spost[i]);
+    if (gate && p.split > 1) store8<float, FORM>(q + 2 * (int64_t)d, at[i], sg[i]);
   }
 }
 
@@ -378,8 +414,16 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const NormArgs a, const Norm
     const float* q = part + (first * 3 + (o < 2 ? o : 2)) * a.d + c;
     float s = 0.f;
     if (c < a.d) {
+      int64_t i = lane;
+      for (; i + 15 * 16 < count; i += 16 * 16) {  // 16 loads on their way at a time, added in their order
+        float v[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) v[u] = q[(i + 16 * u) * 3 * a.d];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) s += v[u];
+      }
 #pragma unroll 4
-      for (int64_t i = lane; i < count; i += 16) s += q[i * 3 * a.d];
+      for (; i < count; i += 16) s += q[i * 3 * a.d];
     }
     red[lane][threadIdx.x & 63] = s;
     __syncthreads();
@@ -395,8 +439,8 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const NormArgs a, const Norm
 }
 
 // ---- launches -------------------------------------------------------------------------------------------------------
-// 8 columns a thread up to 512 threads, 16 beyond
-int threads_of(int d) { return d <= 4096 ? (d + 511) / 512 * 64 : (d + 1023) / 1024 * 64; }
+// 8 columns a thread up to 1024 threads, 16 beyond
+int threads_of(int d) { return d <= 8192 ? (d + 511) / 512 * 64 : (d + 1023) / 1024 * 64; }
 
 NormPlan plan_of(int T, int d, int gate_tokens) {
   // workgroups of about 10 waves a CU (256 CUs) in one round, a few tokens each at least (the sums of a chunk are as many
@@ -419,17 +463,6 @@ NormPlan plan_of(int T, int d, int gate_tokens) {
   return p;
 }
 
-bool al16(const void* p, int64_t ld, size_t e) { return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * (int64_t)e % 16 == 0); }
-
-int form_of(const NormArgs& a) {
-  const size_t r = dtype_size(a.res_dt), v = dtype_size(a.act_dt);
-  const bool wide = a.d % 8 == 0 &&
-      al16(a.h, a.ldh, r) && al16(a.h_out, a.ldh, r) && al16(a.dh_out, a.ldh, r) && al16(a.dh, a.ldh, r) &&
-      al16(a.y, a.ldy, v) && al16(a.dy, a.ldy, v) && al16(a.gate, a.ldg, v) && al16(a.dgate, a.ldg, v) &&
-      al16(a.x, a.ldx, v) && al16(a.dx, a.ldx, v) && al16(a.w_post, 0, 4) && al16(a.w_pre, 0, 4);
-  return !wide ? SINGLE : a.d == 8 * threads_of(a.d) ? EXACT : WIDE;
-}
-
 template <int M, int V, int F, int P> struct Form { static constexpr int MAXT = M, VPT = V, FORM = F, PARTS = P; };
 template <class F> void by_types(const NormArgs& a, F f) {
   if (a.res_dt == BF16) {
@@ -438,27 +471,20 @@ template <class F> void by_types(const NormArgs& a, F f) {
     if (a.act_dt == BF16) f(float(), __bf16()); else f(float(), float());
   }
 }
-template <int FORM, class F> void by_parts(const NormArgs& a, bool all, F f) {
-  if (!all) f(Form<512, 1, FORM, PARTS_ANY>());
-  else if (a.w_post && a.gate) f(Form<512, 1, FORM, PARTS_POST | PARTS_GATE>());
-  else if (a.w_post) f(Form<512, 1, FORM, PARTS_POST>());
-  else if (a.gate) f(Form<512, 1, FORM, PARTS_GATE>());
-  else f(Form<512, 1, FORM, 0>());
+template <int MAXT, int FORM, class F> void by_parts(const NormArgs& a, bool all, F f) {
+  if (!all) f(Form<MAXT, 1, FORM, PARTS_ANY>());
+  else if (a.w_post && a.gate) f(Form<MAXT, 1, FORM, PARTS_POST | PARTS_GATE>());
+  else if (a.w_post) f(Form<MAXT, 1, FORM, PARTS_POST>());
+  else if (a.gate) f(Form<MAXT, 1, FORM, PARTS_GATE>());
+  else f(Form<MAXT, 1, FORM, 0>());
 }
 // all: every part but post norm and gate is given
 template <class F> hipError_t by_form(const NormArgs& a, bool all, F f) {
-  const int form = form_of(a);
-  if (a.d > 8192) {
-    if (form == SINGLE) f(Form<1024, 2, SINGLE, PARTS_ANY>()); else f(Form<1024, 2, WIDE, PARTS_ANY>());
-  } else if (a.d > 4096) {
-    if (form == SINGLE) f(Form<512, 2, SINGLE, PARTS_ANY>()); else f(Form<512, 2, WIDE, PARTS_ANY>());
-  } else if (form == EXACT) {
-    by_parts<EXACT>(a, all, f);
-  } else if (form == WIDE) {
-    by_parts<WIDE>(a, all, f);
-  } else {
-    by_parts<SINGLE>(a, all, f);
-  }
+  if (a.d < 8) f(Form<512, 1, SINGLE, PARTS_ANY>());
+  else if (a.d > 8192) f(Form<1024, 2, WIDE, PARTS_ANY>());
+  else if (a.d > 4096) by_parts<1024, WIDE>(a, all, f);
+  else if (a.d % 512 == 0) by_parts<512, EXACT>(a, all, f);
+  else by_parts<512, WIDE>(a, all, f);
   return hipGetLastError();
 }
 

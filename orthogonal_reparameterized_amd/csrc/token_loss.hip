@@ -939,7 +939,9 @@ dim3 grid_of(int64_t n) { return dim3((unsigned)std::min<int64_t>(n, kMaxBlocks)
 template <int A, int B> struct Size { static constexpr int NT = A, VPT = B; };
 template <class T, class F> void by_size(int steps, int64_t groups, F f) {
   const bool few = groups < 512;
-  if (steps <= 512) f(T(), Size<256, 2>());
+  if (!few && steps <= 128) f(T(), Size<64, 2>());
+  else if (!few && steps <= 512) f(T(), Size<64, 8>());
+  else if (steps <= 512) f(T(), Size<256, 2>());
   else if (steps <= 1024) f(T(), Size<256, 4>());
   else if (!few && steps <= 2048) f(T(), Size<256, 8>());
   else if (!few && steps <= 4096) f(T(), Size<256, 16>());
