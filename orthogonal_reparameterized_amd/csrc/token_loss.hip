@@ -198,24 +198,30 @@ template <class T, int NT, int VPT> struct Held {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) asm volatile("" : "+v"(d[i]));
   }
-  __device__ __forceinline__ float max() const {
+  // Where step i and all behind it are nobody's: a pass ends there (uniform; looked at a quarter of the steps at a time)
+  static __device__ __forceinline__ bool done(const Steps<T>& s, int i) {
+    return VPT >= 4 && i > 0 && i % (VPT / 4) == 0 && i * NT >= s.steps;
+  }
+  __device__ __forceinline__ float max(const Steps<T>& s) const {
     float m = x;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < VPT; ++i) {
+      if (done(s, i)) break;
 #pragma unroll
       for (int k = 0; k < Vec<T>::N; k += 2) m = max3(m, Vec<T>::get(d[i], k), Vec<T>::get(d[i], k + 1));
+    }
     return m;
   }
 };
 
-constexpr int kSlots = 32;   // threads whose steps are looked through at a time
+constexpr int kSlots = 64;   // threads whose steps are looked through at a time
 template <int NT, int VPT> struct Shared {
   float m[NT / 64], z[NT / 64], s[NT / 64];
   float tmax[NT];           // each thread's largest logit
   uint16_t slot[NT];        // its place among the threads that can hold one of the best; 0xffff: it cannot
   u32x4 held[VPT][kSlots];  // steps of the threads of kSlots such places
   int first[kSlots];        // and which threads they are
-  uint64_t cand[kCand];
+  alignas(16) uint64_t cand[kCand + 2];
   uint64_t best[NT / 64];
   float tau;
   int nwin, ncand;
@@ -289,13 +295,18 @@ __device__ void best_of(const Held<T, NT, VPT>& h, const Steps<T>& s, int base, 
         }
       }
       __syncthreads();
-      const int nc = sh.ncand;
+      const int nc = min(sh.ncand, kCand + 1);
+      if (tid == 0) sh.cand[min(nc, kCand)] = 0;  // read in pairs
+      __syncthreads();
       sure = nc >= K && nc <= kCand;
       if (sure) {
         for (int c = tid; c < nc; c += NT) {
           const uint64_t key = sh.cand[c];
           int rank = 0;
-          for (int o = 0; o < nc; ++o) rank += sh.cand[o] > key;
+          for (int o = 0; o < nc; o += 2) {
+            const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(&sh.cand[o]);
+            rank += (k2.x > key) + (k2.y > key);
+          }
           if (rank < K) out(rank, key);
         }
       }
@@ -404,7 +415,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
     h.load(s);
     const int id = sp.nseg == 1 ? token_of(a, row) : -1;
     const float z_id = id >= 0 ? (float)z[id] : 0.f;  // before the gradient may overwrite it
-    const float tmax = h.max();
+    const float tmax = h.max(s);
     float m = wave_max(tmax);
     if (lane == 0) sh.m[wave] = m;
     __syncthreads();
@@ -416,6 +427,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
     h.repack();
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      if (h.done(s, i)) break;
       float zi = 0.f, si = 0.f;
 #pragma unroll
       for (int k = 0; k < Vec<T>::N; ++k) {
@@ -465,6 +477,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
       const int t0 = lane_id();
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
+        if (h.done(s, i)) break;
         const int v = t0 + i * NT;
         float f[Vec<T>::N];
         g.template step<T>(h.d[i], s.first(v), f);
@@ -720,6 +733,7 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
     if (tid < 32 && bits[NT * VPT / 4] >> tid & 1) h.x = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      if (h.done(s, i)) break;
       const uint32_t b = reinterpret_cast<const uint8_t*>(bits)[tid + i * NT];
       if (b) {
 #pragma unroll
@@ -727,7 +741,7 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
           if (b >> k & 1) Vec<T>::none(h.d[i], k);
       }
     }
-    float mt = wave_max(h.max());
+    float mt = wave_max(h.max(s));
     if (lane == 0) sm[wave] = mt;
     __syncthreads();
     mt = sm[0];
@@ -738,6 +752,7 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
     h.repack();
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      if (h.done(s, i)) break;
       float zi = 0.f;
 #pragma unroll
       for (int k = 0; k < Vec<T>::N; ++k) zi += exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
@@ -773,6 +788,7 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
       const int t0 = lane_id();
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
+        if (h.done(s, i)) break;
         const int v = t0 + i * NT;
         float f[Vec<T>::N];
 #pragma unroll
@@ -940,6 +956,7 @@ template <int A, int B> struct Size { static constexpr int NT = A, VPT = B; };
 template <class T, class F> void by_size(int steps, int64_t groups, F f) {
   const bool few = groups < 512;
   if (!few && steps <= 128) f(T(), Size<64, 2>());
+  else if (!few && steps <= 256) f(T(), Size<64, 4>());
   else if (!few && steps <= 512) f(T(), Size<64, 8>());
   else if (steps <= 512) f(T(), Size<256, 2>());
   else if (steps <= 1024) f(T(), Size<256, 4>());
