@@ -401,33 +401,47 @@ __global__ __launch_bounds__(MAXT, MAXT <= 512 ? 3 : 4) void k_norm_bwd(const No
   }
 }
 
-// Adds the chunks' sums: y = 0, 1: all chunks into dw_pre, dw_post; y = 2 + r: the chunks of gate row r (stored as TA).
-// 64 columns a workgroup, 16 threads a column that take every 16th chunk, in a fixed order.
+// Adds the chunks' sums in a fixed order, 64 columns and 16 threads a column in a workgroup. y = 0, 1: all chunks into
+// dw_pre, dw_post, every 16th chunk a thread. y >= 2: the gate rows' chunks (stored as TA), a row a workgroup the same way
+// where a row has many, else a row a thread (per_thread).
 template <class TA>
-__global__ __launch_bounds__(1024) void k_norm_sums(const NormArgs a, const NormPlan p, const float* part, int rows) {
+__global__ __launch_bounds__(1024) void k_norm_sums(const NormArgs a, const NormPlan p, const float* part, int rows,
+                                                    bool per_thread) {
   __shared__ float red[16][64];
   const int c = blockIdx.x * 64 + (threadIdx.x & 63), lane = threadIdx.x >> 6;
-  for (int64_t o = blockIdx.y; o < 2 + rows; o += gridDim.y) {
-    const bool skip = (o == 0 && !a.dw_pre) || (o == 1 && !a.dw_post);  // uniform
-    if (skip) continue;
+  const int64_t pitch = 3 * (int64_t)a.d, units = per_thread ? (rows + 15) / 16 : rows;
+  const bool in = c < a.d;
+  for (int64_t o = blockIdx.y; o < 2 + units; o += gridDim.y) {
+    if ((o == 0 && !a.dw_pre) || (o == 1 && !a.dw_post)) continue;  // uniform
+    if (o >= 2 && per_thread) {
+      const int64_t r = (o - 2) * 16 + lane;
+      if (r < rows && in) {
+        const float* q = part + r * p.split * pitch + 2 * (int64_t)a.d + c;
+        float s = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < p.split; ++i) s += q[i * pitch];
+        ((TA*)a.dgate)[r * a.ldg + c] = (TA)s;
+      }
+      continue;
+    }
     const int64_t first = o < 2 ? 0 : (o - 2) * p.split, count = o < 2 ? p.chunks : p.split;
-    const float* q = part + (first * 3 + (o < 2 ? o : 2)) * a.d + c;
+    const float* q = part + first * pitch + (o < 2 ? o : 2) * a.d + c;
     float s = 0.f;
-    if (c < a.d) {
+    if (in) {
       int64_t i = lane;
       for (; i + 15 * 16 < count; i += 16 * 16) {  // 16 loads on their way at a time, added in their order
         float v[16];
 #pragma unroll
-        for (int u = 0; u < 16; ++u) v[u] = q[(i + 16 * u) * 3 * a.d];
+        for (int u = 0; u < 16; ++u) v[u] = q[(i + 16 * u) * pitch];
 #pragma unroll
         for (int u = 0; u < 16; ++u) s += v[u];
       }
 #pragma unroll 4
-      for (; i < count; i += 16) s += q[i * 3 * a.d];
+      for (; i < count; i += 16) s += q[i * pitch];
     }
     red[lane][threadIdx.x & 63] = s;
     __syncthreads();
-    if (lane == 0 && c < a.d) {
+    if (lane == 0 && in) {
 #pragma unroll
       for (int i = 1; i < 16; ++i) s += red[i][threadIdx.x];
       if (o == 0) a.dw_pre[c] = s;
@@ -528,9 +542,10 @@ hipError_t launch_norm_bwd(const NormArgs& a, void* ws, hipStream_t st) {
   const int rows = p.split > 1 ? (a.T + p.run - 1) / p.run : 0;
   if (!a.dw_pre && !a.dw_post && rows == 0) return hipSuccess;
   ProfScope prof(POET_K_NORM, st, 0, (double)p.chunks * 2 * a.d * 4);
-  const dim3 grid((a.d + 63) / 64, std::min(2 + rows, 65535));
-  if (a.act_dt == BF16) hipLaunchKernelGGL(k_norm_sums<__bf16>, grid, dim3(1024), 0, st, a, p, part, rows);
-  else hipLaunchKernelGGL(k_norm_sums<float>, grid, dim3(1024), 0, st, a, p, part, rows);
+  const bool per_thread = p.split <= 64;
+  const dim3 grid((a.d + 63) / 64, std::min(2 + (per_thread ? (rows + 15) / 16 : rows), 65535));
+  if (a.act_dt == BF16) hipLaunchKernelGGL(k_norm_sums<__bf16>, grid, dim3(1024), 0, st, a, p, part, rows, per_thread);
+  else hipLaunchKernelGGL(k_norm_sums<float>, grid, dim3(1024), 0, st, a, p, part, rows, per_thread);
   return hipGetLastError();
 }
 

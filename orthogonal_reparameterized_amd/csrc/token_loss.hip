@@ -715,7 +715,15 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
     Held<T, NT, VPT> h;
     h.load(s);
     for (int i = tid; i <= NT * VPT / 4; i += NT) bits[i] = 0;
-    if (wave == 0) teach<T>(L, a, z, raw);
+    if (wave == 0) {
+      if (sp.nseg == 1) {
+        teach<T>(L, a, z, raw);
+      } else {  // a segment needs the places only
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (lane + 64 * u < a.K) L.id[lane + 64 * u] = raw.id[u] >= 0 && raw.id[u] < a.V ? raw.id[u] : -1;
+      }
+    }
     __syncthreads();
     if (wave == 0) {
       bool twice = false;
