@@ -9,6 +9,7 @@
 // and best alternatives a second launch joins; their gradient is a launch of its own.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/poet.h"
 #include "internal.h"
@@ -21,7 +22,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr float kLow = -1.0e30f;  // stands in for -inf where it would meet a zero factor, and survives a gradient times it
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kMaxBlocks = 1 << 20;  // workgroups of one launch; they stride over the rest
-constexpr int kCand = 512;           // candidates for the best alternatives that one workgroup keeps
 
 // ---- 16-byte steps of a row ----------------------------------------------------------------------------------
 // A row of n elements is up to N-1 elements before the first 16-byte boundary, steps of N elements from there, and up to
@@ -214,78 +214,93 @@ template <class T, int NT, int VPT> struct Held {
   }
 };
 
-constexpr int kSlots = 64;   // threads whose steps are looked through at a time
-template <int NT, int VPT> struct Shared {
-  float m[NT / 64], z[NT / 64], s[NT / 64];
-  float tmax[NT];           // each thread's largest logit
-  uint16_t slot[NT];        // its place among the threads that can hold one of the best; 0xffff: it cannot
-  u32x4 held[VPT][kSlots];  // steps of the threads of kSlots such places
-  int first[kSlots];        // and which threads they are
-  alignas(16) uint64_t cand[kCand + 2];
+// A workgroup's threads in at most 256 groups of adjacent ones (more would only make the search among them longer)
+template <int NT> struct Partials { float m[NT / 64], z[NT / 64], s[NT / 64]; };
+template <int NT, int VPT> struct Shared : Partials<NT> {
+  static constexpr int G = NT > 256 ? NT / 256 : 1, kGroups = NT / G;
+  static constexpr int kSlots = NT < 256 ? 16 : 64;    // groups whose steps are looked through at a time
+  static constexpr int kCand = NT < 256 ? 256 : 1024;  // candidates
+  float gmax[kGroups];             // each group's largest logit
+  uint16_t slot[kGroups];          // its place among those that can hold one of the best; 0xffff: it cannot
+  u32x4 held[VPT][kSlots * G];     // the steps of kSlots groups
+  int first[kSlots * G];           // and whose they are
+  alignas(16) uint64_t cand[kCand];
   uint64_t best[NT / 64];
+  int count[NT / 64];
   float tau;
   int nwin, ncand;
 };
 
-// The K best alternatives of a row or segment of n elements, ranked, as out(rank, key).
-// Threads' own maxima bound them: with tau the K-th largest of those, K elements are >= tau, and an element >= tau sits
-// with a thread whose maximum is >= tau. One wave finds tau bit by bit and numbers those threads, a little over K of them;
-// they leave their steps in LDS, where all threads look through them (a scan of the registers would cost every wave all
-// its steps, reading the elements again a trip to memory a thread), and the few >= tau are ranked against each other.
-// Rows where that is not few (many ties, fewer threads with logits than K), or that hold a NaN, are read again K times.
+// The K best alternatives of a row or segment of n elements, ranked, as out(rank, key). K <= kGroups.
+// The groups' own maxima bound them: with tau the K-th largest of those, K elements are >= tau, and an element >= tau sits
+// with a group whose maximum is. One wave finds tau bit by bit and numbers those groups, a little over K of them; they
+// leave their steps in LDS, where all threads look through them (a scan of the registers would cost every wave all its
+// steps, reading the elements again a trip to memory a group), and the few >= tau are ranked against each other.
+// Where they are not few, many tokens are equal (or all that are left are -inf): then tau is found exactly, the elements
+// > tau are taken the same way, and the first of those equal to it by reading the row from its beginning. What neither
+// fits (a NaN, hundreds of the best logits in one group) is read again K times.
 template <class T, int NT, int VPT, class Out>
-__device__ void best_of(const Held<T, NT, VPT>& h, const Steps<T>& s, int base, int n, int K, float tmax, bool sure,
+__device__ void best_of(const Held<T, NT, VPT>& h, const Steps<T>& s, int base, int n, int K, float tmax, bool numbers,
                         Shared<NT, VPT>& sh, Out out) {
-  constexpr int N = Vec<T>::N;
+  typedef Shared<NT, VPT> S;
+  constexpr int N = Vec<T>::N, G = S::G, W = S::kGroups / 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if (sure) {  // uniform
-    sh.tmax[tid] = tmax;
+  if (numbers) {  // uniform, as are the conditions below
+    float gm = tmax;
+    if constexpr (G == 4) {
+      gm = fmaxf(gm, dpp<0xB1, 0xf>(gm, gm));  // quad_perm 1 0 3 2, 2 3 0 1
+      gm = fmaxf(gm, dpp<0x4E, 0xf>(gm, gm));
+    }
+    if (tid % G == 0) sh.gmax[tid / G] = gm;
     __syncthreads();
-    if (wave == 0) {
-      uint32_t key[NT / 64], t = 0;
+    const auto pass = [&](auto is_exact) {
+      constexpr bool exact = decltype(is_exact)::value;
+      if (wave == 0) {
+        uint32_t key[W], t = 0;
 #pragma unroll
-      for (int q = 0; q < NT / 64; ++q) key[q] = ordered(sh.tmax[q * 64 + lane]);
-      // bf16 logits differ in the upper 16 bits only; 10 bits less than float32's 32 let in a few threads more
-      for (int bit = 31; bit >= (N == 8 ? 16 : 10); --bit) {
-        const uint32_t c = t | 1u << bit;
+        for (int q = 0; q < W; ++q) key[q] = ordered(sh.gmax[q * 64 + lane]);
+        // at first: bf16 logits differ in the upper 16 bits only; 10 bits less than float32's 32 let in a few groups more
+        for (int bit = 31; bit >= (exact ? 0 : N == 8 ? 16 : 10); --bit) {
+          const uint32_t c = t | 1u << bit;
+          int m = 0;
+#pragma unroll
+          for (int q = 0; q < W; ++q) m += __popcll(__ballot(key[q] >= c));
+          if (m >= K) t = c;
+          if (m == K && !exact) break;
+        }
         int m = 0;
 #pragma unroll
-        for (int q = 0; q < NT / 64; ++q) m += __popcll(__ballot(key[q] >= c));
-        if (m >= K) t = c;
-        if (m == K) break;
+        for (int q = 0; q < W; ++q) {
+          const bool in = exact ? key[q] > t : key[q] >= t;
+          const uint64_t b = __ballot(in);
+          sh.slot[q * 64 + lane] = in ? (uint16_t)(m + __popcll(b & ((1ull << lane) - 1))) : (uint16_t)0xffff;
+          m += __popcll(b);
+        }
+        if (lane == 0) { sh.nwin = m; sh.ncand = 0; sh.tau = unordered(t); }
       }
-      int m = 0;
-#pragma unroll
-      for (int q = 0; q < NT / 64; ++q) {
-        const uint64_t b = __ballot(key[q] >= t);
-        sh.slot[q * 64 + lane] = key[q] >= t ? (uint16_t)(m + __popcll(b & ((1ull << lane) - 1))) : (uint16_t)0xffff;
-        m += __popcll(b);
-      }
-      if (lane == 0) { sh.nwin = m; sh.ncand = 0; sh.tau = unordered(t); }
-    }
-    __syncthreads();
-    const float tau = sh.tau;
-    const int nwin = sh.nwin, slot = sh.slot[tid];
-    sure = tau > -INFINITY && nwin <= 2 * K + 64;
-    if (sure) {
+      __syncthreads();
+      const float tau = sh.tau;
+      const int nwin = sh.nwin, slot = sh.slot[tid / G];
+      if (!exact && !(tau > -INFINITY && nwin <= K + K / 2 + 32)) return false;
       const auto take = [&](float z, int j) {
-        if (z >= tau) {
+        if (exact ? z > tau : z >= tau) {
           const int c = atomicAdd(&sh.ncand, 1);
-          if (c < kCand) sh.cand[c] = rank_key(z, base + j);
+          if (c < S::kCand) sh.cand[c] = rank_key(z, base + j);
         }
       };
       if (tid < s.singles) take(h.x, s.single(tid));
-      for (int w0 = 0; w0 < nwin; w0 += kSlots) {
+      for (int w0 = 0; w0 < nwin; w0 += S::kSlots) {
         if (w0 > 0) __syncthreads();
-        if (slot >= w0 && slot < w0 + kSlots) {
+        if (slot >= w0 && slot < w0 + S::kSlots) {
+          const int at = (slot - w0) * G + tid % G;
 #pragma unroll
-          for (int i = 0; i < VPT; ++i) sh.held[i][slot - w0] = h.d[i];
-          sh.first[slot - w0] = tid;
+          for (int i = 0; i < VPT; ++i) sh.held[i][at] = h.d[i];
+          sh.first[at] = tid;
         }
         __syncthreads();
-        const int ns = min(kSlots, nwin - w0);
-        for (int u = tid; u < VPT * kSlots; u += NT) {
-          const int w = u % kSlots, i = u / kSlots;
+        const int ns = min(S::kSlots, nwin - w0) * G;
+        for (int u = tid; u < VPT * S::kSlots * G; u += NT) {
+          const int w = u % (S::kSlots * G), i = u / (S::kSlots * G);
           if (w >= ns) continue;
           const int v = sh.first[w] + i * NT;
           if (v >= s.steps) continue;
@@ -295,24 +310,45 @@ __device__ void best_of(const Held<T, NT, VPT>& h, const Steps<T>& s, int base, 
         }
       }
       __syncthreads();
-      const int nc = min(sh.ncand, kCand + 1);
-      if (tid == 0) sh.cand[min(nc, kCand)] = 0;  // read in pairs
-      __syncthreads();
-      sure = nc >= K && nc <= kCand;
-      if (sure) {
-        for (int c = tid; c < nc; c += NT) {
-          const uint64_t key = sh.cand[c];
-          int rank = 0;
-          for (int o = 0; o < nc; o += 2) {
-            const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(&sh.cand[o]);
-            rank += (k2.x > key) + (k2.y > key);
+      if (exact && sh.ncand < K) {  // the first of those equal to tau
+        int have = sh.ncand;
+        for (int j0 = 0; j0 < n && have < K; j0 += NT) {
+          const int j = j0 + tid;
+          const float z = j < n ? (float)s.p[j] : 0.f;
+          const bool eq = j < n && z == tau;
+          const uint64_t b = __ballot(eq);
+          if (lane == 0) sh.count[wave] = __popcll(b);
+          __syncthreads();
+          int at = have;
+#pragma unroll
+          for (int q = 0; q < NT / 64; ++q) {
+            if (q < wave) at += sh.count[q];
+            have += sh.count[q];
           }
-          if (rank < K) out(rank, key);
+          at += __popcll(b & ((1ull << lane) - 1));
+          if (eq && at < K) sh.cand[at] = rank_key(z, base + j);
+          __syncthreads();
         }
+        if (tid == 0) sh.ncand = min(have, K);
+        __syncthreads();
       }
-    }
+      const int nc = sh.ncand;
+      if (nc < K || nc > S::kCand) return false;
+      for (int c = tid; c < nc; c += NT) {
+        const uint64_t key = sh.cand[c];
+        int rank = nc & 1 ? sh.cand[nc - 1] > key : 0;
+        for (int o = 0; o < nc - 1; o += 2) {
+          const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(&sh.cand[o]);
+          rank += (k2.x > key) + (k2.y > key);
+        }
+        if (rank < K) out(rank, key);
+      }
+      return true;
+    };
+    if (pass(std::false_type())) return;
+    __syncthreads();  // all have read what the second pass begins with
+    if (pass(std::true_type())) return;
   }
-  if (sure) return;
   uint64_t last = ~0ull;
   for (int k = 0; k < K; ++k) {
     uint64_t best = 0;
@@ -400,9 +436,9 @@ struct RowGrad {
 
 // One workgroup a row (nseg == 1: results, and the gradient where asked) or a segment of a row (partials into `part`:
 // m, Z, S, -, then the K best keys).
-template <class T, int NT, int VPT>
+template <class T, int NT, int VPT, bool TOP>
 __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const RowSplit sp) {
-  __shared__ Shared<NT, VPT> sh;
+  __shared__ typename std::conditional<TOP, Shared<NT, VPT>, Partials<NT>>::type sh;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   for (int64_t w = blockIdx.x; w < (int64_t)a.T * sp.nseg; w += gridDim.x) {
     const int64_t row = sp.nseg == 1 ? w : w / sp.nseg;
@@ -457,7 +493,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
       if (part) { part[0] = m; part[1] = Z; part[2] = S; }
       else write_row(a, row, r, z_id, id);
     }
-    if (a.K > 0) {
+    if constexpr (TOP) {
       best_of<T, NT, VPT>(h, s, base, n, min(a.K, n), tmax, Z == Z, sh, [&](int k, uint64_t key) {
         if (part) {
           reinterpret_cast<uint64_t*>(part + 4)[k] = key;
@@ -470,7 +506,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
         for (int k = n + tid; k < a.K; k += NT) reinterpret_cast<uint64_t*>(part + 4)[k] = 0;  // a short last segment
     }
     if (a.dz) {
-      if (a.K > 0) __syncthreads();  // the alternatives may be read from memory: before the gradient in place
+      if (TOP) __syncthreads();  // the alternatives may be read from memory: before the gradient in place
       T* dz = (T*)a.dz + row * a.ldd;
       const RowGrad g(a, row, id, m, r.logZ, r.H);
       h.repack();
@@ -961,11 +997,11 @@ dim3 grid_of(int64_t n) { return dim3((unsigned)std::min<int64_t>(n, kMaxBlocks)
 
 // f(type, threads, steps a thread) for the smallest workgroup that holds `steps`
 template <int A, int B> struct Size { static constexpr int NT = A, VPT = B; };
-template <class T, class F> void by_size(int steps, int64_t groups, F f) {
+template <class T, class F> void by_size(int steps, int64_t groups, int K, F f) {
   const bool few = groups < 512;
-  if (!few && steps <= 128) f(T(), Size<64, 2>());
-  else if (!few && steps <= 256) f(T(), Size<64, 4>());
-  else if (!few && steps <= 512) f(T(), Size<64, 8>());
+  if (!few && K <= 32 && steps <= 128) f(T(), Size<64, 2>());
+  else if (!few && K <= 32 && steps <= 256) f(T(), Size<64, 4>());
+  else if (!few && K <= 32 && steps <= 512) f(T(), Size<64, 8>());
   else if (steps <= 512) f(T(), Size<256, 2>());
   else if (steps <= 1024) f(T(), Size<256, 4>());
   else if (!few && steps <= 2048) f(T(), Size<256, 8>());
@@ -997,9 +1033,10 @@ hipError_t launch_logprobs(const TokenArgs& args, float* part, hipStream_t st) {
     ProfScope prof(POET_K_HEAD, st, n * (a.dz ? 9 : 6), n * e * (a.dz ? 2 : 1));
     const int64_t groups = (int64_t)a.T * sp.nseg;
     by_type(a.dt, [&](auto t) {
-      by_size<decltype(t)>(sp.steps, groups, [&](auto u, auto z) {
+      by_size<decltype(t)>(sp.steps, groups, a.K, [&](auto u, auto z) {
         using Z = decltype(z);
-        hipLaunchKernelGGL((k_logprobs<decltype(u), Z::NT, Z::VPT>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
+        if (a.K > 0) hipLaunchKernelGGL((k_logprobs<decltype(u), Z::NT, Z::VPT, true>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
+        else hipLaunchKernelGGL((k_logprobs<decltype(u), Z::NT, Z::VPT, false>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
       });
     });
   }
@@ -1036,7 +1073,7 @@ hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
     ProfScope prof(POET_K_HEAD, st, n * (a.dz ? 7 : 4), n * e * (a.dz ? 2 : 1));
     const int64_t groups = (int64_t)a.T * sp.nseg;
     by_type(a.dt, [&](auto t) {
-      by_size<decltype(t)>(sp.steps, groups, [&](auto u, auto z) {
+      by_size<decltype(t)>(sp.steps, groups, 0, [&](auto u, auto z) {
         using Z = decltype(z);
         hipLaunchKernelGGL((k_distill<decltype(u), Z::NT, Z::VPT>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
       });
