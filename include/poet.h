@@ -401,15 +401,14 @@ poet_status poet_singular_value_entropy(int32_t m, int32_t n, const float* W, in
 /* ---- the model's answer: token log-probabilities and distillation ----------------------------------------
  * What the last linear's output is scored and trained by (the evaluation by perplexity of the Key results; the token
  * loss whose gradient is the head's dY). Each row of logits z [T x V] (row pitch ld, float32 or bf16) is a distribution
- *     p = softmax(s z),  s = inv_temp (finite, > 0),
+ *     p = softmax(s z),  s = inv_temp (1e-30 to 1e30),
  * computed in float32 with sums over the row's distance to its maximum m. A row may hold -inf (tokens that cannot
  * come); a row that holds nothing else has log-probabilities -inf, entropy 0 and gradient 0. A row that holds a NaN or
  * +inf gives NaN in its float32 results and its gradient. Values are bit-identical from call to call.
  * The logits and their gradient keep their padding columns [V, ld) untouched. dlogits may be the logits themselves (in
  * place: same address and pitch); otherwise the two must not overlap (checked: POET_E_ARG). T == 0 does nothing.
  * V up to POET_MAX_VOCAB (POET_E_UNSUPPORTED above).
- * ws: at least the matching *_workspace_bytes bytes (0, and ws may be NULL, for most sizes: rows that one workgroup
- * holds). Calls that share a workspace must be ordered on one stream or by events, as must captured graphs. */
+ * ws: at least the matching *_workspace_bytes bytes (0, and ws may be NULL, for rows up to 64 KB). Calls that share a workspace must be ordered on one stream or by events, as must captured graphs. */
 #define POET_MAX_VOCAB (1 << 24)
 #define POET_MAX_TOP 128 /* largest K: alternatives of a row, entries of a teacher's list */
 typedef struct poet_logits {
@@ -462,7 +461,7 @@ poet_status poet_token_logprobs_bwd(const poet_logits* L, const void* logits, co
 enum { POET_DISTILL_RENORM = 0, POET_DISTILL_TAIL = 1 };
 typedef struct poet_teacher {
   int32_t K, mode;
-  float inv_temp; /* finite, > 0 */
+  float inv_temp; /* 1e-30 to 1e30 */
 } poet_teacher;
 size_t poet_distill_workspace_bytes(int32_t T, int32_t V, int32_t dtype);
 poet_status poet_distill(const poet_logits* L, const poet_teacher* teacher, const void* logits, const int32_t* t_ids,

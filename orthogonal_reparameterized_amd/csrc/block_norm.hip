@@ -456,23 +456,25 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const NormArgs a, const Norm
 // 8 columns a thread up to 1024 threads, 16 beyond
 int threads_of(int d) { return d <= 8192 ? (d + 511) / 512 * 64 : (d + 1023) / 1024 * 64; }
 
+int up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
 NormPlan plan_of(int T, int d, int gate_tokens) {
   // workgroups of about 10 waves a CU (256 CUs) in one round, a few tokens each at least (the sums of a chunk are as many
   // bytes as 3 to 6 of a token's rows), but at most 256 tokens in a row of float32 additions
   const int groups = 256 * std::max(1, 10 / (threads_of(d) / 64));
-  const int len = std::min(256, std::max(std::min(T, 2), (T + groups - 1) / groups));
+  const int len = (int)std::min<int64_t>(256, std::max(std::min(T, 2), up(T, groups)));
   NormPlan p;
   p.len = len;
   const int run = std::min(gate_tokens, T);
   if (run > len) {
-    const int runs = (T + run - 1) / run;
-    p.split = std::min((run + len - 1) / len, std::max({1, groups / runs, (run + 255) / 256}));
-    p.len = (run + p.split - 1) / p.split;
+    const int runs = up(T, run);
+    p.split = std::min(up(run, len), std::max({1, groups / runs, up(run, 256)}));
+    p.len = up(run, p.split);
     p.run = run;
     p.chunks = runs * p.split;
   } else {
     if (run > 1) p.len = len / run * run;
-    p.chunks = (T + p.len - 1) / p.len;
+    p.chunks = up(T, p.len);
   }
   return p;
 }
@@ -504,7 +506,7 @@ template <class F> hipError_t by_form(const NormArgs& a, bool all, F f) {
 
 double moved(const NormArgs& a, int res, int act) {
   const double n = (double)a.T * a.d;
-  const double rows = a.gate ? (double)((a.T + a.gate_tokens - 1) / a.gate_tokens) : 0;
+  const double rows = a.gate ? (double)up(a.T, a.gate_tokens) : 0;
   return n * res * dtype_size(a.res_dt) + n * act * dtype_size(a.act_dt) + rows * a.d * dtype_size(a.act_dt);
 }
 
@@ -539,7 +541,7 @@ hipError_t launch_norm_bwd(const NormArgs& a, void* ws, hipStream_t st) {
     });
     if (e != hipSuccess) return e;
   }
-  const int rows = p.split > 1 ? (a.T + p.run - 1) / p.run : 0;
+  const int rows = p.split > 1 ? up(a.T, p.run) : 0;
   if (!a.dw_pre && !a.dw_post && rows == 0) return hipSuccess;
   ProfScope prof(POET_K_NORM, st, 0, (double)p.chunks * 2 * a.d * 4);
   const bool per_thread = p.split <= 64;

@@ -2214,6 +2214,7 @@ poet_status poet_merge_group(int32_t count, const poet_layer* layers, float* con
 // ---- the model's answer: rows of logits ------------------------------------------------------------------------
 
 static bool finite_pos(float x) { return x > 0.f && x - x == 0.f; }
+static bool temp_ok(float x) { return x >= 1e-30f && x <= 1e30f; }
 
 // Whether two row-strided regions (rows of w bytes at pitch p from base) share a byte. Regions of one pitch may be
 // interleaved columns of one buffer; any other crossing of address ranges counts as an overlap.
@@ -2239,7 +2240,7 @@ static bool logits_info(const poet_logits* L) {
   if (L->V > POET_MAX_VOCAB) return fail(POET_E_UNSUPPORTED, "V = %d > %d", L->V, POET_MAX_VOCAB), false;
   if (L->ld < L->V) return fail(POET_E_SHAPE, "ld = %lld too small for V = %d", (long long)L->ld, L->V), false;
   if (!rows_fit(L->T, L->ld)) return fail(POET_E_UNSUPPORTED, "ld = %lld too large", (long long)L->ld), false;
-  if (!finite_pos(L->inv_temp)) return fail(POET_E_ARG, "inv_temp = %g must be finite and > 0", L->inv_temp), false;
+  if (!temp_ok(L->inv_temp)) return fail(POET_E_ARG, "inv_temp = %g must be in [1e-30, 1e30]", L->inv_temp), false;
   return true;
 }
 
@@ -2315,7 +2316,7 @@ static bool teacher_info(const poet_teacher* t, const float* t_lse) {
   if (!t) return fail(POET_E_ARG, "null teacher"), false;
   if (t->K < 1 || t->K > POET_MAX_TOP) return fail(POET_E_SHAPE, "K = %d must be in [1, %d]", t->K, POET_MAX_TOP), false;
   if (t->mode != POET_DISTILL_RENORM && t->mode != POET_DISTILL_TAIL) return fail(POET_E_ARG, "bad mode %d", t->mode), false;
-  if (!finite_pos(t->inv_temp)) return fail(POET_E_ARG, "teacher inv_temp = %g must be finite and > 0", t->inv_temp), false;
+  if (!temp_ok(t->inv_temp)) return fail(POET_E_ARG, "teacher inv_temp = %g must be in [1e-30, 1e30]", t->inv_temp), false;
   if (t->mode == POET_DISTILL_RENORM && t_lse) return fail(POET_E_ARG, "t_lse goes with POET_DISTILL_TAIL"), false;
   return true;
 }

@@ -2,7 +2,7 @@
 // alternatives of each row of logits, the distillation loss on a teacher's top logits, and the gradients of both.
 //
 // With z a row of V logits, s = inv_temp, m = max z, d = z - m, Z = sum exp(s d):
-//   log p_j = s d_j - log Z,   entropy H = log Z - (s/Z) sum exp(s d) d   (both sums have one sign: nothing cancels).
+//   log p_j = s d_j - log Z,   entropy H = log Z - (1/Z) sum exp(s d) s d   (both sums have one sign: nothing cancels).
 // Both operators and their gradients are bound by HBM: a row is read once (and its gradient written once), so one
 // workgroup keeps a whole row in registers, 16 bytes a thread and step, and every pass over it (maximum, sums, best
 // alternatives, gradient) reads those. Rows beyond a workgroup's registers are split into segments whose maxima, sums
@@ -19,8 +19,11 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr float kLow = -1.0e30f;  // stands in for -inf where it would meet a zero factor, and survives a gradient times it
 constexpr float kLog2e = 1.44269504088896340736f;
+// The exponent t = s (z - m) log2(e) stands next to e = 2^t in the entropy's terms. Where e is 0 anyway, t is cut off
+// here, so that a logit of -inf gives 0 and no gradient overflows on the way to it.
+constexpr float kLow = -200.f;
+constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kMaxBlocks = 1 << 20;  // workgroups of one launch; they stride over the rest
 
 // ---- 16-byte steps of a row ----------------------------------------------------------------------------------
@@ -368,16 +371,16 @@ __device__ void best_of(const Held<T, NT, VPT>& h, const Steps<T>& s, int base, 
 }
 
 // ---- log-probabilities --------------------------------------------------------------------------------------------
-// a row's results from its maximum m, Z = sum exp(s (z - m)) and S = sum exp(s (z - m)) (z - m)
+// a row's results from its maximum m, Z = sum e and S = sum e t, e = 2^t, t = s (z - m) log2(e)
 struct RowStat {
   float m, ref, logZ, H;
   bool none;  // every logit is -inf (a NaN would be in Z)
-  __device__ RowStat(float m_, float Z, float S, float s) {
+  __device__ RowStat(float m_, float Z, float S) {
     m = m_;
     none = m == -INFINITY && Z == 0.f;
     ref = m == -INFINITY ? 0.f : m;
     logZ = logf(Z);
-    H = none ? 0.f : logZ - s * S / Z;
+    H = none ? 0.f : logZ - kLn2 * S / Z;
   }
   __device__ __forceinline__ float logp(float z, float s) const { return none ? -INFINITY : (z - ref) * s - logZ; }
 };
@@ -394,7 +397,7 @@ __device__ void write_row(const TokenArgs& a, int64_t row, const RowStat& r, flo
   if (a.logp) a.logp[row] = id < 0 ? 0.f : r.logp(z_id, a.s);
 }
 
-// The gradient of one row's logits is e (A + B d) with e = exp(s d), d = z - m, plus gl s at the token:
+// The gradient of one row's logits is e (A + B t), plus gl s at the token:
 //   dz = s (gl (delta - p) - gh p (log p + H)),  p = e / Z,  log p = s d - log Z.
 struct RowGrad {
   float c, ref, A, B, gl;
@@ -409,18 +412,18 @@ struct RowGrad {
     c = a.s * kLog2e;
     const float inv = expf(-logZ) * a.s;
     A = -inv * (gl + gh * (H - logZ));
-    B = -inv * gh * a.s;
+    B = -inv * gh * kLn2;
     gl *= a.s;
   }
   __device__ __forceinline__ float one(float z, int j) const {
-    const float d = z - ref;
-    return zero ? 0.f : exp2_fast(d * c) * fmaf(B, fmaxf(d, kLow), A) + (j == id ? gl : 0.f);
+    const float t = (z - ref) * c;
+    return zero ? 0.f : exp2_fast(t) * fmaf(B, fmaxf(t, kLow), A) + (j == id ? gl : 0.f);
   }
   template <class T> __device__ __forceinline__ void step(const u32x4& v, int j0, float* f) const {
 #pragma unroll
     for (int k = 0; k < Vec<T>::N; ++k) {
-      const float d = Vec<T>::get(v, k) - ref;
-      f[k] = exp2_fast(d * c) * fmaf(B, fmaxf(d, kLow), A);
+      const float t = (Vec<T>::get(v, k) - ref) * c;
+      f[k] = exp2_fast(t) * fmaf(B, fmaxf(t, kLow), A);
     }
     if ((unsigned)(id - j0) < (unsigned)Vec<T>::N) {
 #pragma unroll
@@ -467,17 +470,17 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
       float zi = 0.f, si = 0.f;
 #pragma unroll
       for (int k = 0; k < Vec<T>::N; ++k) {
-        const float d = Vec<T>::get(h.d[i], k) - ref, e = exp2_fast(d * c);
+        const float t = (Vec<T>::get(h.d[i], k) - ref) * c, e = exp2_fast(t);
         zi += e;
-        si = fmaf(e, fmaxf(d, kLow), si);
+        si = fmaf(e, fmaxf(t, kLow), si);
       }
       Z += zi;
       S += si;
     }
     {
-      const float d = h.x - ref, e = exp2_fast(d * c);
+      const float t = (h.x - ref) * c, e = exp2_fast(t);
       Z += e;
-      S = fmaf(e, fmaxf(d, kLow), S);
+      S = fmaf(e, fmaxf(t, kLow), S);
     }
     Z = wave_sum(Z);
     S = wave_sum(S);
@@ -487,7 +490,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
     S = sh.s[0];
 #pragma unroll
     for (int q = 1; q < NT / 64; ++q) { Z += sh.z[q]; S += sh.s[q]; }
-    const RowStat r(m, Z, S, a.s);
+    const RowStat r(m, Z, S);
     float* part = sp.nseg > 1 ? sp.part + w * sp.stride : nullptr;
     if (tid == 0) {
       if (part) { part[0] = m; part[1] = Z; part[2] = S; }
@@ -538,14 +541,14 @@ __global__ __launch_bounds__(256) void k_logprobs_join(const TokenArgs a, const 
     for (int q = lane; q < sp.nseg; q += 64) {
       const float* p = part + q * sp.stride;
       if (p[0] == -INFINITY && p[1] == 0.f) continue;
-      // S of the segment is about its own maximum mq: sum e (z - m) = f (S + Z (mq - m)), f = exp(s (mq - m))
-      const float dm = (p[0] == -INFINITY ? 0.f : p[0]) - ref, f = exp2f(dm * a.s * kLog2e);
+      // S of the segment is about its own maximum: with t its exponent about the row's, sum e t = 2^t (S + Z t)
+      const float t = ((p[0] == -INFINITY ? 0.f : p[0]) - ref) * (a.s * kLog2e), f = exp2f(t);
       Z += (double)f * p[1];
-      S += (double)f * (p[2] + (double)p[1] * fmaxf(dm, kLow));
+      S += (double)f * (p[2] + (double)p[1] * fmaxf(t, kLow));
     }
     Z = wave_sum(Z);
     S = wave_sum(S);
-    const RowStat r(m, (float)Z, (float)S, a.s);
+    const RowStat r(m, (float)Z, (float)S);
     if (tid == 0) {
       const int id = token_of(a, row);
       const float z_id = id < 0 ? 0.f

@@ -47,7 +47,8 @@ def _dis_bwd(L=None, K=5, mode=0, tit=1.0, z=Z, ti=TI, tz=TL, lse=None, st=ST, w
 BAD_LOGITS = [(dict(T=-1), B.POET_E_SHAPE), (dict(V=0), B.POET_E_SHAPE), (dict(ld=999), B.POET_E_SHAPE),
               (dict(V=B.POET_MAX_VOCAB + 1, ld=1 << 25), B.POET_E_UNSUPPORTED), (dict(ld=1 << 47), B.POET_E_UNSUPPORTED),
               (dict(dtype=2), B.POET_E_DTYPE), (dict(inv_temp=0.0), B.POET_E_ARG), (dict(inv_temp=-1.0), B.POET_E_ARG),
-              (dict(inv_temp=float("nan")), B.POET_E_ARG), (dict(inv_temp=float("inf")), B.POET_E_ARG)]
+              (dict(inv_temp=float("nan")), B.POET_E_ARG), (dict(inv_temp=float("inf")), B.POET_E_ARG),
+              (dict(inv_temp=2e30), B.POET_E_ARG), (dict(inv_temp=5e-31), B.POET_E_ARG)]
 
 
 @pytest.mark.parametrize("over,status", BAD_LOGITS)

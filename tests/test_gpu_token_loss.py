@@ -314,6 +314,87 @@ def test_distill_lists(V, dt, tail):
         check_distill(zt2, z2, full, lq + 1e-3, tail=True, w=w, dt=dt)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [90, 700, 1500, 3000, 7000, 15001, 30000])
+def test_many_rows(V, dt):
+    """Enough rows that each gets the smallest workgroup that holds it."""
+    T, K = 530, 17
+    announce(f"many rows V={V} {dt}")
+    rng = np.random.default_rng(V)
+    z = gauss(T, V, 12)
+    z[:, rng.random(V) < 0.05] = -INF
+    z[7] = -INF
+    z[8, 3:] = -INF
+    z[9] = np.round(z[9])
+    zt, z, _ = rows(z, dt, 1 if V % 2 else 0)
+    ids = rng.integers(-1, V, T)
+    check_logprobs(zt, z, ids, K=K, gl=rng.standard_normal(T), gh=rng.standard_normal(T), dt=dt)
+    check_logprobs(zt, z, ids, s=1.5, gl=rng.standard_normal(T), dt=dt)
+    t_ids, t_z, lse = teacher(np.where(np.isfinite(z), z, -50.0), K, V)
+    t_ids[5, 4:9] = t_ids[5, 0]
+    t_ids[6] = -1
+    w = rng.standard_normal(T)
+    for tail in (False, True):
+        check_distill(zt, z, t_ids, t_z, tail=tail, lse=lse + 0.2 if tail else None, w=w, dt=dt)
+
+
+def test_more_rows_than_workgroups():
+    """More rows than one launch has workgroups."""
+    T, V, P = 1_100_003, 9, 7
+    announce("more rows than workgroups")
+    base, t = gauss(P, V, 13), torch.arange(T, device="cuda") % P
+    zt = torch.as_tensor(base, dtype=torch.float32).cuda()[t].contiguous()
+    ids = (t % V).to(torch.int32)
+    one = torch.ones(T, device="cuda")
+    o = dict(logp=torch.empty(T, device="cuda"), stats=torch.empty((T, 4), device="cuda"), entropy=torch.empty(T, device="cuda"),
+             top_ids=torch.empty((T, 3), dtype=torch.int32, device="cuda"), top_logp=torch.empty((T, 3), device="cuda"),
+             dlogits=torch.empty_like(zt))
+    B().poet_token_logprobs(zt, ids, dlogp=one, dentropy=one, **o)
+    d = dict(loss=torch.empty(T, device="cuda"), stats=torch.empty((T, 4), device="cuda"), dlogits=torch.empty_like(zt))
+    B().poet_distill(zt, o["top_ids"], o["top_logp"], mode=1, dloss=one, **d)
+    again = torch.empty_like(zt)
+    B().poet_token_logprobs_bwd(zt, ids, o["stats"], one, again, dentropy=one)
+    torch.cuda.synchronize()
+    assert torch.equal(again, o["dlogits"])
+    # rows of an odd pitch lie at four alignments, where their sums are taken in different orders: every row is held to
+    # the formula with the bounds of tests/token_ref.py
+    z64, n, t = zt[:P].double().cpu().numpy(), np.arange(P), t.cpu().numpy()
+    lp, _, H = R.logprobs(z64)
+    bound = lambda r: R.DZ + 4 * R.U * np.abs(r)  # noqa: E731
+    idp = ids.cpu().numpy()
+    close(o["logp"], lp[t, idp], bound(lp[t, idp]), "logp")
+    close(o["entropy"], H[t], R.entropy_bound(z64)[t], "entropy")
+    at = R.top(z64, 3)
+    np.testing.assert_array_equal(o["top_ids"].cpu().numpy(), at[t])
+    tl = np.take_along_axis(lp, at, 1)
+    close(o["top_logp"], tl[t], bound(tl)[t], "top_logp")
+    for k in range(V):  # the gradients of the rows whose token is k
+        sel = np.flatnonzero(idp == k)[:1000]
+        ref, err = R.logprobs_grad(z64[t[sel]], 1.0, idp[sel], np.ones(len(sel)), np.ones(len(sel)))
+        close(o["dlogits"][torch.as_tensor(sel).cuda()], ref, err + R.U * np.abs(ref) + 1e-38, "dlogits")
+    sel = np.r_[0:500, T - 500:T]
+    ref, err, dref, derr = R.distill(z64[t[sel]], 1.0, at[t[sel]], o["top_logp"].double().cpu().numpy()[sel], 1.0, True, None,
+                                     np.ones(len(sel)))
+    close(d["loss"][torch.as_tensor(sel).cuda()], ref, err + 2 * R.U * np.abs(ref), "loss")
+    close(d["dlogits"][torch.as_tensor(sel).cuda()], dref, derr + R.U * np.abs(dref) + 1e-38, "dlogits of the distillation")
+
+
+@pytest.mark.parametrize("s", [1e-30, 1e-3, 300.0, 1e30])
+def test_extreme_temperatures_and_gradients(s):
+    """Temperatures at the ends of their range, upstream gradients of 1e20, masked logits: finite, and the formula's."""
+    T, V = 4, 600
+    announce(f"temperature {s}")
+    rng = np.random.default_rng(3)
+    z = gauss(T, V, 14)
+    z[:, ::3] = -INF
+    z[1, ::3] = -3e38
+    zt, z, _ = rows(z, "f32")
+    big = 1e20 if s < 1e10 else 1.0
+    gl, gh = f32(big * rng.standard_normal(T)), f32(big * rng.standard_normal(T))
+    check_logprobs(zt, z, np.array([1, 2, 4, -1]), s=float(np.float32(s)), gl=gl.double().cpu().numpy(),
+                   gh=gh.double().cpu().numpy())
+
+
 def test_gradients_against_differences():
     """Both gradients against central differences of the float64 formulas along random directions."""
     T, V, K, s, e = 4, 61, 9, 0.8, 1e-5
