@@ -437,92 +437,121 @@ struct RowGrad {
   }
 };
 
+// Adds the earlier parts' sums, about their own maximum m0, to a part's Z and S about ref
+__device__ __forceinline__ void add_part(float& Z, float& S, float ref, float m0, float Z0, float S0, float c) {
+  if (m0 == -INFINITY && Z0 == 0.f) return;
+  const float t = ((m0 == -INFINITY ? 0.f : m0) - ref) * c, e = exp2_fast(t);
+  Z = fmaf(e, Z0, Z);
+  S += e * fmaf(Z0, fmaxf(t, kLow), S0);
+}
+
 // One workgroup a row (nseg == 1: results, and the gradient where asked) or a segment of a row (partials into `part`:
-// m, Z, S, -, then the K best keys).
-template <class T, int NT, int VPT, bool TOP>
+// m, Z, S, -, then the K best keys). LOOP: a row in sp.loops parts, one after another; the last one stays in the registers
+// for its gradient, the others are read again.
+template <class T, int NT, int VPT, bool TOP, bool LOOP>
 __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const RowSplit sp) {
   __shared__ typename std::conditional<TOP, Shared<NT, VPT>, Partials<NT>>::type sh;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   for (int64_t w = blockIdx.x; w < (int64_t)a.T * sp.nseg; w += gridDim.x) {
     const int64_t row = sp.nseg == 1 ? w : w / sp.nseg;
     const int seg = sp.nseg == 1 ? 0 : (int)(w - row * sp.nseg);
-    const int base = seg * sp.len;
     const T* z = (const T*)a.z + row * a.ld;
-    const int n = min(sp.len, a.V - base);
-    const Steps<T> s(z + base, n);
+    int base = seg * sp.len, n = min(sp.len, a.V - base);
+    Steps<T> s(z + base, n);
     Held<T, NT, VPT> h;
     h.load(s);
     const int id = sp.nseg == 1 ? token_of(a, row) : -1;
     const float z_id = id >= 0 ? (float)z[id] : 0.f;  // before the gradient may overwrite it
-    const float tmax = h.max(s);
-    float m = wave_max(tmax);
-    if (lane == 0) sh.m[wave] = m;
-    __syncthreads();
-    m = sh.m[0];
+    const float c = a.s * kLog2e;
+    float tmax, m, Z, S, before_m = -INFINITY, before_Z = 0.f, before_S = 0.f;  // before: of the parts so far
+    for (int part = 0;;) {
+      tmax = h.max(s);
+      m = wave_max(tmax);
+      if (lane == 0) sh.m[wave] = m;
+      __syncthreads();
+      m = sh.m[0];
 #pragma unroll
-    for (int q = 1; q < NT / 64; ++q) m = fmaxf(m, sh.m[q]);
-    const float ref = m == -INFINITY ? 0.f : m, c = a.s * kLog2e;
-    float Z = 0.f, S = 0.f;
-    h.repack();
+      for (int q = 1; q < NT / 64; ++q) m = fmaxf(m, sh.m[q]);
+      if (LOOP) m = fmaxf(m, before_m);
+      const float ref = m == -INFINITY ? 0.f : m;
+      Z = S = 0.f;
+      h.repack();
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      if (h.done(s, i)) break;
-      float zi = 0.f, si = 0.f;
+      for (int i = 0; i < VPT; ++i) {
+        if (h.done(s, i)) break;
+        float zi = 0.f, si = 0.f;
 #pragma unroll
-      for (int k = 0; k < Vec<T>::N; ++k) {
-        const float t = (Vec<T>::get(h.d[i], k) - ref) * c, e = exp2_fast(t);
-        zi += e;
-        si = fmaf(e, fmaxf(t, kLow), si);
+        for (int k = 0; k < Vec<T>::N; ++k) {
+          const float t = (Vec<T>::get(h.d[i], k) - ref) * c, e = exp2_fast(t);
+          zi += e;
+          si = fmaf(e, fmaxf(t, kLow), si);
+        }
+        Z += zi;
+        S += si;
       }
-      Z += zi;
-      S += si;
-    }
-    {
-      const float t = (h.x - ref) * c, e = exp2_fast(t);
-      Z += e;
-      S = fmaf(e, fmaxf(t, kLow), S);
-    }
-    Z = wave_sum(Z);
-    S = wave_sum(S);
-    if (lane == 0) { sh.z[wave] = Z; sh.s[wave] = S; }
-    __syncthreads();
-    Z = sh.z[0];
-    S = sh.s[0];
+      {
+        const float t = (h.x - ref) * c, e = exp2_fast(t);
+        Z += e;
+        S = fmaf(e, fmaxf(t, kLow), S);
+      }
+      Z = wave_sum(Z);
+      S = wave_sum(S);
+      if (lane == 0) { sh.z[wave] = Z; sh.s[wave] = S; }
+      __syncthreads();
+      Z = sh.z[0];
+      S = sh.s[0];
 #pragma unroll
-    for (int q = 1; q < NT / 64; ++q) { Z += sh.z[q]; S += sh.s[q]; }
+      for (int q = 1; q < NT / 64; ++q) { Z += sh.z[q]; S += sh.s[q]; }
+      if (!LOOP) break;
+      add_part(Z, S, ref, before_m, before_Z, before_S, c);
+      if (++part == sp.loops) break;
+      before_m = m; before_Z = Z; before_S = S;
+      base = part * sp.len;
+      n = min(sp.len, a.V - base);
+      s = Steps<T>(z + base, n);
+      h.load(s);
+    }
     const RowStat r(m, Z, S);
-    float* part = sp.nseg > 1 ? sp.part + w * sp.stride : nullptr;
+    float* out = sp.nseg > 1 ? sp.part + w * sp.stride : nullptr;
     if (tid == 0) {
-      if (part) { part[0] = m; part[1] = Z; part[2] = S; }
+      if (out) { out[0] = m; out[1] = Z; out[2] = S; }
       else write_row(a, row, r, z_id, id);
     }
     if constexpr (TOP) {
       best_of<T, NT, VPT>(h, s, base, n, min(a.K, n), tmax, Z == Z, sh, [&](int k, uint64_t key) {
-        if (part) {
-          reinterpret_cast<uint64_t*>(part + 4)[k] = key;
+        if (out) {
+          reinterpret_cast<uint64_t*>(out + 4)[k] = key;
         } else {
           a.top_ids[row * a.K + k] = (int)~(uint32_t)key;
           a.top_logp[row * a.K + k] = r.logp(unordered((uint32_t)(key >> 32)), a.s);
         }
       });
-      if (part)
-        for (int k = n + tid; k < a.K; k += NT) reinterpret_cast<uint64_t*>(part + 4)[k] = 0;  // a short last segment
+      if (out)
+        for (int k = n + tid; k < a.K; k += NT) reinterpret_cast<uint64_t*>(out + 4)[k] = 0;  // a short last segment
     }
     if (a.dz) {
       if (TOP) __syncthreads();  // the alternatives may be read from memory: before the gradient in place
       T* dz = (T*)a.dz + row * a.ldd;
-      const RowGrad g(a, row, id, m, r.logZ, r.H);
-      h.repack();
-      const int t0 = lane_id();
+      RowGrad g(a, row, id, m, r.logZ, r.H);
+      if (LOOP) g.id = id < 0 ? INT32_MIN : id - base;  // in the part's own count
+      for (int part = LOOP ? sp.loops - 1 : 0;;) {
+        h.repack();
+        const int t0 = lane_id();
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        if (h.done(s, i)) break;
-        const int v = t0 + i * NT;
-        float f[Vec<T>::N];
-        g.template step<T>(h.d[i], s.first(v), f);
-        if (v < s.steps) s.store(dz, v, f);
+        for (int i = 0; i < VPT; ++i) {
+          if (h.done(s, i)) break;
+          const int v = t0 + i * NT;
+          float f[Vec<T>::N];
+          g.template step<T>(h.d[i], s.first(v), f);
+          if (v < s.steps) s.store(dz + (LOOP ? base : 0), v, f);
+        }
+        if (tid < s.singles) dz[s.single(tid) + (LOOP ? base : 0)] = (T)g.one(h.x, s.single(tid));
+        if (!LOOP || --part < 0) break;
+        base = part * sp.len;
+        if (id >= 0) g.id = id - base;
+        s = Steps<T>(z + base, min(sp.len, a.V - base));
+        h.load(s);
       }
-      if (tid < s.singles) dz[s.single(tid)] = (T)g.one(h.x, s.single(tid));
     }
     __syncthreads();  // the next row's shared values
   }
@@ -736,7 +765,7 @@ __device__ __forceinline__ float grad_listed(const List& L, int k, float s) {
 }
 
 // One workgroup a row or segment, as k_logprobs; partials: mt, Zt.
-template <class T, int NT, int VPT>
+template <class T, int NT, int VPT, bool LOOP>
 __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowSplit sp) {
   __shared__ List L;
   __shared__ float sm[NT / 64], sz[NT / 64];
@@ -745,15 +774,13 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
   for (int64_t w = blockIdx.x; w < (int64_t)a.T * sp.nseg; w += gridDim.x) {
     const int64_t row = sp.nseg == 1 ? w : w / sp.nseg;
     const int seg = sp.nseg == 1 ? 0 : (int)(w - row * sp.nseg);
-    const int base = seg * sp.len;
     const T* z = (const T*)a.z + row * a.ld;
-    const int n = min(sp.len, a.V - base);
-    const Steps<T> s(z + base, n);
+    int base = seg * sp.len, n = min(sp.len, a.V - base);
+    Steps<T> s(z + base, n);
     ListRaw raw;
     if (wave == 0) raw = fetch_list(a, row);
     Held<T, NT, VPT> h;
     h.load(s);
-    for (int i = tid; i <= NT * VPT / 4; i += NT) bits[i] = 0;
     if (wave == 0) {
       if (sp.nseg == 1) {
         teach<T>(L, a, z, raw);
@@ -763,51 +790,70 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
           if (lane + 64 * u < a.K) L.id[lane + 64 * u] = raw.id[u] >= 0 && raw.id[u] < a.V ? raw.id[u] : -1;
       }
     }
-    __syncthreads();
-    if (wave == 0) {
-      bool twice = false;
-      for (int k = lane; k < a.K; k += 64) {
-        const int j = L.id[k] - base;
-        if (L.id[k] < 0 || j < 0 || j >= n) continue;
-        const int at = j - s.head, v = at / Vec<T>::N;
-        const bool step = at >= 0 && v < s.steps;
-        const uint32_t b = 1u << (step ? v % 4 * 8 + at % Vec<T>::N : at < 0 ? j : j - s.steps * Vec<T>::N);
-        twice |= (atomicOr(&bits[step ? v / 4 : NT * VPT / 4], b) & b) != 0;
+    const float c = a.s * kLog2e;
+    float mt, Z, before_m = -INFINITY, before_Z = 0.f;  // before: of the parts so far
+    for (int part = 0;;) {
+      for (int i = tid; i <= NT * VPT / 4; i += NT) bits[i] = 0;
+      __syncthreads();
+      if (wave == 0) {
+        bool twice = false;
+        for (int k = lane; k < a.K; k += 64) {
+          const int j = L.id[k] - base;
+          if (L.id[k] < 0 || j < 0 || j >= n) continue;
+          const int at = j - s.head, v = at / Vec<T>::N;
+          const bool step = at >= 0 && v < s.steps;
+          const uint32_t b = 1u << (step ? v % 4 * 8 + at % Vec<T>::N : at < 0 ? j : j - s.steps * Vec<T>::N);
+          twice |= (atomicOr(&bits[step ? v / 4 : NT * VPT / 4], b) & b) != 0;
+        }
+        if (__any(twice) && lane == 0) L.repeated = 1;
       }
-      if (__any(twice) && lane == 0) L.repeated = 1;
-    }
-    __syncthreads();
-    if (tid < 32 && bits[NT * VPT / 4] >> tid & 1) h.x = -INFINITY;
+      __syncthreads();
+      if (tid < 32 && bits[NT * VPT / 4] >> tid & 1) h.x = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      if (h.done(s, i)) break;
-      const uint32_t b = reinterpret_cast<const uint8_t*>(bits)[tid + i * NT];
-      if (b) {
+      for (int i = 0; i < VPT; ++i) {
+        if (h.done(s, i)) break;
+        const uint32_t b = reinterpret_cast<const uint8_t*>(bits)[tid + i * NT];
+        if (b) {
 #pragma unroll
-        for (int k = 0; k < Vec<T>::N; ++k)
-          if (b >> k & 1) Vec<T>::none(h.d[i], k);
+          for (int k = 0; k < Vec<T>::N; ++k)
+            if (b >> k & 1) Vec<T>::none(h.d[i], k);
+        }
       }
+      mt = wave_max(h.max(s));
+      if (lane == 0) sm[wave] = mt;
+      __syncthreads();
+      mt = sm[0];
+#pragma unroll
+      for (int q = 1; q < NT / 64; ++q) mt = fmaxf(mt, sm[q]);
+      if (LOOP) mt = fmaxf(mt, before_m);
+      const float ref = mt == -INFINITY ? 0.f : mt;
+      Z = 0.f;
+      h.repack();
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        if (h.done(s, i)) break;
+        float zi = 0.f;
+#pragma unroll
+        for (int k = 0; k < Vec<T>::N; ++k) zi += exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
+        Z += zi;
+      }
+      Z = wave_sum(Z + exp2_fast((h.x - ref) * c));
+      if (lane == 0) sz[wave] = Z;
+      __syncthreads();
+      if (!LOOP) break;
+      Z = sz[0];
+#pragma unroll
+      for (int q = 1; q < NT / 64; ++q) Z += sz[q];
+      float none = 0.f;
+      add_part(Z, none, ref, before_m, before_Z, 0.f, c);
+      if (++part == sp.loops) break;
+      before_m = mt; before_Z = Z;
+      base = part * sp.len;
+      n = min(sp.len, a.V - base);
+      s = Steps<T>(z + base, n);
+      h.load(s);
     }
-    float mt = wave_max(h.max(s));
-    if (lane == 0) sm[wave] = mt;
-    __syncthreads();
-    mt = sm[0];
-#pragma unroll
-    for (int q = 1; q < NT / 64; ++q) mt = fmaxf(mt, sm[q]);
-    const float ref = mt == -INFINITY ? 0.f : mt, c = a.s * kLog2e;
-    float Z = 0.f;
-    h.repack();
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      if (h.done(s, i)) break;
-      float zi = 0.f;
-#pragma unroll
-      for (int k = 0; k < Vec<T>::N; ++k) zi += exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
-      Z += zi;
-    }
-    Z = wave_sum(Z + exp2_fast((h.x - ref) * c));
-    if (lane == 0) sz[wave] = Z;
-    __syncthreads();
+    const float ref = mt == -INFINITY ? 0.f : mt;
     if (sp.nseg > 1) {
       if (tid == 0) {
         double Zt = 0;
@@ -820,8 +866,9 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
       continue;
     }
     if (wave == 0) {
-      double Zt = 0;
-      for (int q = 0; q < NT / 64; ++q) Zt += sz[q];
+      double Zt = LOOP ? (double)Z : 0;
+      if (!LOOP)
+        for (int q = 0; q < NT / 64; ++q) Zt += sz[q];
       if (L.repeated) join_repeated(L, a.K);
       finish_distill(L, a, row, mt, Zt);
       if (a.dz && lane == 0) grad_factors(L, a);
@@ -831,18 +878,24 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
       T* dz = (T*)a.dz + row * a.ldd;
       const float C = L.C;
       const bool zero = L.scale == 0.f;
-      h.repack();
-      const int t0 = lane_id();
+      for (int part = LOOP ? sp.loops - 1 : 0;;) {
+        h.repack();
+        const int t0 = lane_id();
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        if (h.done(s, i)) break;
-        const int v = t0 + i * NT;
-        float f[Vec<T>::N];
+        for (int i = 0; i < VPT; ++i) {
+          if (h.done(s, i)) break;
+          const int v = t0 + i * NT;
+          float f[Vec<T>::N];
 #pragma unroll
-        for (int k = 0; k < Vec<T>::N; ++k) f[k] = zero ? 0.f : C * exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
-        if (v < s.steps) s.store(dz, v, f);
+          for (int k = 0; k < Vec<T>::N; ++k) f[k] = zero ? 0.f : C * exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
+          if (v < s.steps) s.store(dz + (LOOP ? base : 0), v, f);
+        }
+        if (tid < s.singles) dz[s.single(tid) + (LOOP ? base : 0)] = (T)(zero ? 0.f : C * exp2_fast((h.x - ref) * c));
+        if (!LOOP || --part < 0) break;
+        base = part * sp.len;
+        s = Steps<T>(z + base, min(sp.len, a.V - base));
+        h.load(s);
       }
-      if (tid < s.singles) dz[s.single(tid)] = (T)(zero ? 0.f : C * exp2_fast((h.x - ref) * c));
       __syncthreads();  // the listed tokens' own, over what the steps wrote there
       if (wave == 0)
         for (int k = lane; k < a.K; k += 64)
@@ -975,15 +1028,23 @@ __global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a,
 
 // ---- launches ----------------------------------------------------------------------------------------------------
 constexpr int kHeld = 1024 * 16;    // steps that the largest workgroup holds
+constexpr int kLoopRows = 200;      // rows from which on long ones are taken by one workgroup each (about the CUs)
 constexpr int kSegment = 256 * 16;  // ... and that the largest of 256 threads holds, four of which share a CU
 
 // How rows of V elements are split over workgroups of `held` steps (a row of at most N-1 elements more than a workgroup's
 // steps goes with those as its single elements, however it is aligned). With its gradient a row stays whole where it can,
-// to be read once (and wherever the gradient is written, so that it is the same); without, segments keep more loads in
-// flight.
-RowSplit split_of(int V, int dt, int K, bool grad) {
-  const int n = dt == BF16 ? 8 : 4, held = grad && V / n <= kHeld ? kHeld : kSegment, cap = held * n;
+// to be read once (and wherever the gradient is written, so that it is the same), and a longer one whole in parts where
+// there are rows enough to keep every CU at one of its own; without, segments keep more loads in flight.
+RowSplit split_of(int T, int V, int dt, int K, bool grad) {
+  const int n = dt == BF16 ? 8 : 4;
   RowSplit sp;
+  if (grad && V / n > kHeld && T >= kLoopRows && K == 0) {
+    sp.loops = (V + kHeld * n - 1) / (kHeld * n);
+    sp.len = ((V + sp.loops - 1) / sp.loops + 63) / 64 * 64;
+    sp.steps = kHeld;
+    return sp;
+  }
+  const int held = grad && V / n <= kHeld ? kHeld : kSegment, cap = held * n;
   if (V / n > held) sp.nseg = (V + cap - 1) / cap;
   sp.len = sp.nseg == 1 ? V : ((V + sp.nseg - 1) / sp.nseg + 63) / 64 * 64;  // <= cap, and whole steps
   sp.stride = 4 + 2 * K;
@@ -1021,14 +1082,14 @@ template <class F> hipError_t by_type(int dt, F f) {
 }  // namespace
 
 size_t logprobs_part_bytes(int T, int V, int dt, int K) {
-  const RowSplit sp = split_of(V, dt, K, false);
+  const RowSplit sp = split_of(T, V, dt, K, false);
   return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
 
 hipError_t launch_logprobs(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  const bool after = a.dz && (a.V / (a.dt == BF16 ? 8 : 4) > kHeld || !same_alignment(a));  // the gradient in its own launch
-  RowSplit sp = split_of(a.V, a.dt, a.K, args.dz);
+  RowSplit sp = split_of(a.T, a.V, a.dt, a.K, args.dz);
+  const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in its own launch
   sp.part = part;
   if (after) a.dz = nullptr;
   {
@@ -1036,10 +1097,15 @@ hipError_t launch_logprobs(const TokenArgs& args, float* part, hipStream_t st) {
     ProfScope prof(POET_K_HEAD, st, n * (a.dz ? 9 : 6), n * e * (a.dz ? 2 : 1));
     const int64_t groups = (int64_t)a.T * sp.nseg;
     by_type(a.dt, [&](auto t) {
-      by_size<decltype(t)>(sp.steps, groups, a.K, [&](auto u, auto z) {
+      using T = decltype(t);
+      if (sp.loops > 1) {
+        hipLaunchKernelGGL((k_logprobs<T, 1024, 16, false, true>), grid_of(groups), dim3(1024), 0, st, a, sp);
+        return;
+      }
+      by_size<T>(sp.steps, groups, a.K, [&](auto, auto z) {
         using Z = decltype(z);
-        if (a.K > 0) hipLaunchKernelGGL((k_logprobs<decltype(u), Z::NT, Z::VPT, true>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
-        else hipLaunchKernelGGL((k_logprobs<decltype(u), Z::NT, Z::VPT, false>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
+        if (a.K > 0) hipLaunchKernelGGL((k_logprobs<T, Z::NT, Z::VPT, true, false>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
+        else hipLaunchKernelGGL((k_logprobs<T, Z::NT, Z::VPT, false, false>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
       });
     });
   }
@@ -1061,14 +1127,14 @@ hipError_t launch_logprobs_bwd(const TokenArgs& a, hipStream_t st) {
 }
 
 size_t distill_part_bytes(int T, int V, int dt) {
-  const RowSplit sp = split_of(V, dt, 0, false);
+  const RowSplit sp = split_of(T, V, dt, 0, false);
   return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
 
 hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  const bool after = a.dz && (a.V / (a.dt == BF16 ? 8 : 4) > kHeld || !same_alignment(a));  // the gradient in its own launch
-  RowSplit sp = split_of(a.V, a.dt, 0, args.dz);
+  RowSplit sp = split_of(a.T, a.V, a.dt, 0, args.dz);
+  const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in its own launch
   sp.part = part;
   if (after) a.dz = nullptr;
   {
@@ -1076,9 +1142,14 @@ hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
     ProfScope prof(POET_K_HEAD, st, n * (a.dz ? 7 : 4), n * e * (a.dz ? 2 : 1));
     const int64_t groups = (int64_t)a.T * sp.nseg;
     by_type(a.dt, [&](auto t) {
-      by_size<decltype(t)>(sp.steps, groups, 0, [&](auto u, auto z) {
+      using T = decltype(t);
+      if (sp.loops > 1) {
+        hipLaunchKernelGGL((k_distill<T, 1024, 16, true>), grid_of(groups), dim3(1024), 0, st, a, sp);
+        return;
+      }
+      by_size<T>(sp.steps, groups, 0, [&](auto, auto z) {
         using Z = decltype(z);
-        hipLaunchKernelGGL((k_distill<decltype(u), Z::NT, Z::VPT>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
+        hipLaunchKernelGGL((k_distill<T, Z::NT, Z::VPT, false>), grid_of(groups), dim3(Z::NT), 0, st, a, sp);
       });
     });
   }

@@ -338,6 +338,37 @@ def test_many_rows(V, dt):
         check_distill(zt, z, t_ids, t_z, tail=tail, lse=lse + 0.2 if tail else None, w=w, dt=dt)
 
 
+@pytest.mark.parametrize("V,dt,pad", [(65541, "f32", 0), (70001, "f32", 3), (131080, "bf16", 0), (140001, "bf16", 1)])
+def test_many_long_rows(V, dt, pad):
+    """Rows longer than a workgroup holds, enough of them that each is taken whole in parts: masks that empty a part or
+    all of a row, a maximum in the first or the last part, lists over both; in place and apart."""
+    T, K = 203, 21
+    announce(f"many long rows V={V} {dt}")
+    rng = np.random.default_rng(V)
+    z = gauss(T, V, 15)
+    z[0, : V // 2 + 100] = -INF
+    z[1, V // 2 - 100:] = -INF
+    z[2] = -INF
+    z[3, 7], z[4, V - 1] = 40.0, 40.0
+    z[5, : V // 2 + 100] -= 300.0
+    zt, z, _ = rows(z, dt, pad)
+    ids = rng.integers(-1, V, T)
+    ids[3], ids[4], ids[6], ids[7] = 7, V - 1, 0, V // 2
+    gl, gh = rng.standard_normal(T), rng.standard_normal(T)
+    _, apart = check_logprobs(zt, z, ids, s=0.8, gl=gl, gh=gh, dt=dt, dz=torch.empty((T, V + 5), dtype=zt.dtype, device="cuda")[:, :V])
+    apart = apart.clone()
+    check_logprobs(zt, z, ids, s=0.8, gl=gl, gh=gh, dt=dt, dz=zt)
+    assert torch.equal(zt, apart)
+    zt.copy_(torch.as_tensor(z))
+    t_ids = rng.integers(0, V, (T, K))
+    t_ids[8, 1:6] = t_ids[8, 0]
+    t_ids[9] = -1
+    t_ids[10, :3] = [0, V - 1, V // 2]
+    t_z, w = rng.standard_normal((T, K)) - 4.0, rng.standard_normal(T)
+    for tail in (False, True):
+        check_distill(zt, z, t_ids, t_z, tail=tail, w=w, dt=dt)
+
+
 def test_more_rows_than_workgroups():
     """More rows than one launch has workgroups."""
     T, V, P = 1_100_003, 9, 7
