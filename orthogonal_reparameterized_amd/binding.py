@@ -828,6 +828,9 @@ def _vec(t, name: str, shape: tuple, dtype, dev: int, required: bool = False):
         if required:
             raise ValueError(f"{name} is required")
         return None
+    if type(t) is _torch_module.Tensor and t.get_device() == dev and t.dtype is dtype and t.shape == shape \
+            and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, _torch().Tensor) or t.get_device() != dev:
         _refuse(t, name, dev)
     if t.dtype != dtype:

@@ -1028,17 +1028,21 @@ __global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a,
 
 // ---- launches ----------------------------------------------------------------------------------------------------
 constexpr int kHeld = 1024 * 16;    // steps that the largest workgroup holds
-constexpr int kLoopRows = 200;      // rows from which on long ones are taken by one workgroup each (about the CUs)
+// Rows from which on long ones go whole, in parts, to one workgroup (a CU) each. It reads them once instead of twice, but
+// loads little ahead and fills the CUs in whole rounds: f32 V = 131071 on 256 CUs, whole against segments and a gradient
+// launch, which read the distillation's list again too: distillation T = 211 70 us : 106, 511 150 : 189, 2048 515 : 654;
+// log-probabilities T = 300 107 : 97, 600 178 : 180, 1000 268 : 286, 2048 517 : 581.
+constexpr int kLoopLogprobs = 512, kLoopDistill = 200;
 constexpr int kSegment = 256 * 16;  // ... and that the largest of 256 threads holds, four of which share a CU
 
 // How rows of V elements are split over workgroups of `held` steps (a row of at most N-1 elements more than a workgroup's
 // steps goes with those as its single elements, however it is aligned). With its gradient a row stays whole where it can,
 // to be read once (and wherever the gradient is written, so that it is the same), and a longer one whole in parts where
 // there are rows enough to keep every CU at one of its own; without, segments keep more loads in flight.
-RowSplit split_of(int T, int V, int dt, int K, bool grad) {
+RowSplit split_of(int V, int dt, int K, bool grad, bool loop) {
   const int n = dt == BF16 ? 8 : 4;
   RowSplit sp;
-  if (grad && V / n > kHeld && T >= kLoopRows && K == 0) {
+  if (loop && grad && V / n > kHeld) {
     sp.loops = (V + kHeld * n - 1) / (kHeld * n);
     sp.len = ((V + sp.loops - 1) / sp.loops + 63) / 64 * 64;
     sp.steps = kHeld;
@@ -1082,13 +1086,13 @@ template <class F> hipError_t by_type(int dt, F f) {
 }  // namespace
 
 size_t logprobs_part_bytes(int T, int V, int dt, int K) {
-  const RowSplit sp = split_of(T, V, dt, K, false);
+  const RowSplit sp = split_of(V, dt, K, false, false);
   return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
 
 hipError_t launch_logprobs(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  RowSplit sp = split_of(a.T, a.V, a.dt, a.K, args.dz);
+  RowSplit sp = split_of(a.V, a.dt, a.K, args.dz, a.K == 0 && a.T >= kLoopLogprobs);
   const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in its own launch
   sp.part = part;
   if (after) a.dz = nullptr;
@@ -1127,13 +1131,13 @@ hipError_t launch_logprobs_bwd(const TokenArgs& a, hipStream_t st) {
 }
 
 size_t distill_part_bytes(int T, int V, int dt) {
-  const RowSplit sp = split_of(T, V, dt, 0, false);
+  const RowSplit sp = split_of(V, dt, 0, false, false);
   return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
 
 hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  RowSplit sp = split_of(a.T, a.V, a.dt, 0, args.dz);
+  RowSplit sp = split_of(a.V, a.dt, 0, args.dz, a.T >= kLoopDistill);
   const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in its own launch
   sp.part = part;
   if (after) a.dz = nullptr;

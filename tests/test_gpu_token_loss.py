@@ -369,6 +369,42 @@ def test_many_long_rows(V, dt, pad):
         check_distill(zt, z, t_ids, t_z, tail=tail, w=w, dt=dt)
 
 
+@pytest.mark.parametrize("V,dt,pad", [(65541, "f32", 0), (131071, "f32", 1), (140001, "bf16", 1)])
+def test_long_rows_whole(V, dt, pad):
+    """The same for the log-probabilities with more rows still (some of them are held to the formula)."""
+    T, H = 515, 12
+    announce(f"long rows whole V={V} {dt}")
+    rng = np.random.default_rng(V)
+    head, tail = gauss(H, V, 16), gauss(3, V, 17)
+    head[0, : V // 2 + 100] = -INF
+    head[1, V // 2 - 100:] = -INF
+    head[2] = -INF
+    head[3, 7], head[4, V - 1] = 40.0, 40.0
+    head[5, : V // 2 + 100] -= 300.0
+    zt = torch.empty((T, V + pad), dtype=tdt(dt), device="cuda")[:, :V]
+    zt.normal_()
+    zt[:H], zt[T - 3:] = torch.as_tensor(head).to(tdt(dt)), torch.as_tensor(tail).to(tdt(dt))
+    sel = np.r_[0:H, T - 3:T]
+    z = zt[torch.as_tensor(sel).cuda()].double().cpu().numpy()
+    ids = rng.integers(-1, V, T)
+    ids[3], ids[4], ids[6], ids[7] = 7, V - 1, 0, V // 2
+    gl, gh = f32(rng.standard_normal(T)), f32(rng.standard_normal(T))
+    logp, Hd, st = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty((T, 4), device="cuda")
+    apart = torch.empty((T, V + 3), dtype=zt.dtype, device="cuda")[:, :V]
+    for dz in (apart, zt):
+        B().poet_token_logprobs(zt, i32(ids), logp, st, inv_temp=0.8, entropy=Hd, dlogp=gl, dentropy=gh, dlogits=dz)
+        torch.cuda.synchronize()
+        lp, _, H64 = R.logprobs(z, 0.8)
+        has = ids[sel] >= 0
+        ref = np.where(has, lp[np.arange(len(sel)), np.where(has, ids[sel], 0)], 0.0)
+        at = torch.as_tensor(sel).cuda()
+        close(logp[at], ref, R.DZ + 4 * R.U * np.abs(np.where(np.isfinite(ref), ref, 0)), "logp")
+        close(Hd[at], H64, R.entropy_bound(z, 0.8), "entropy")
+        ref, err = R.logprobs_grad(z, 0.8, ids[sel], gl.double().cpu().numpy()[sel], gh.double().cpu().numpy()[sel])
+        close(dz[at], ref, err + R.HALF[dt] * np.abs(ref) * 1.01 + 1e-38, "dlogits")
+    assert torch.equal(zt, apart)
+
+
 def test_more_rows_than_workgroups():
     """More rows than one launch has workgroups."""
     T, V, P = 1_100_003, 9, 7
