@@ -408,7 +408,8 @@ poet_status poet_singular_value_entropy(int32_t m, int32_t n, const float* W, in
  * The logits and their gradient keep their padding columns [V, ld) untouched. dlogits may be the logits themselves (in
  * place: same address and pitch); otherwise the two must not overlap (checked: POET_E_ARG). T == 0 does nothing.
  * V up to POET_MAX_VOCAB (POET_E_UNSUPPORTED above).
- * ws: at least the matching *_workspace_bytes bytes (0, and ws may be NULL, for rows up to 64 KB). Calls that share a workspace must be ordered on one stream or by events, as must captured graphs. */
+ * ws: at least the matching *_workspace_bytes bytes (0, and ws may be NULL, for rows up to 64 KB; what T rows need is
+ * enough for fewer). Calls that share a workspace must be ordered on one stream or by events, as must captured graphs. */
 #define POET_MAX_VOCAB (1 << 24)
 #define POET_MAX_TOP 128 /* largest K: alternatives of a row, entries of a teacher's list */
 typedef struct poet_logits {

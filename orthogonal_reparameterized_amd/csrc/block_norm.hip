@@ -459,9 +459,11 @@ int threads_of(int d) { return d <= 8192 ? (d + 511) / 512 * 64 : (d + 1023) / 1
 int up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 NormPlan plan_of(int T, int d, int gate_tokens) {
-  // workgroups of about 10 waves a CU (256 CUs) in one round, a few tokens each at least (the sums of a chunk are as many
-  // bytes as 3 to 6 of a token's rows), but at most 256 tokens in a row of float32 additions
-  const int groups = 256 * std::max(1, 10 / (threads_of(d) / 64));
+  // Workgroups of 6 waves a CU (256 CUs) in one round, 10 where a row is one short wave's (32768 tokens, d = 512: 65 us with
+  // 6, 70 with 10; 1377: 162 and 164; 64: 45 and 38; with 3 84, 222 and 66), two tokens each at least (the sums of a
+  // chunk are as many bytes as 3 to 6 of a token's rows; 1001x1377: 1 to 4 tokens within 0.2 us, 8 0.4 us more), but at
+  // most 256 tokens in a row of float32 additions.
+  const int groups = 256 * std::max(1, (d <= 256 ? 10 : 6) / (threads_of(d) / 64));
   const int len = (int)std::min<int64_t>(256, std::max(std::min(T, 2), up(T, groups)));
   NormPlan p;
   p.len = len;
@@ -517,7 +519,10 @@ size_t block_norm_bytes(int T, int d, int gate_tokens) { return (size_t)plan_of(
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st) {
   ProfScope prof(POET_K_NORM, st, 10.0 * a.T * a.d, moved(a, a.y ? 2 : 1, (a.y ? 1 : 0) + (a.x ? 1 : 0)));
   const int nt = threads_of(a.d);
-  const int grid = std::min(a.T, 256 * std::max(1, 2048 / nt));
+  // More workgroups than the CUs hold, so that none waits for the last round, but few enough that the weights are read for
+  // several tokens: 16384x2048 64.6 us, with 2048 threads a CU 67.0; 16384x2560 81.5 : 86.4; 32768x512 34.6 : 34.9, with
+  // 8192 35.7; 8192x5461, whose workgroups of 1024 threads have the most weights, 102.2 with 2048, 106.1 with 4096
+  const int grid = std::min(a.T, 256 * ((nt > 512 ? 2048 : nt >= 256 ? 8192 : 4096) / nt));
   return by_form(a, a.y && a.x, [&](auto form) {
     using F = decltype(form);
     by_types(a, [&](auto r, auto v) {

@@ -313,6 +313,7 @@ struct TokenArgs {
   const float* dloss = nullptr; float* loss = nullptr;
   float* stats = nullptr;
   void* dz = nullptr; int64_t ldd = 0;
+  bool stream = false;  // past the caches (set by the launches)
 };
 // Rows in nseg segments of len elements (1: whole rows): segment q of row t leaves its partials at part + (t nseg + q)
 // stride floats; a segment is `steps` 16-byte steps at most. loops > 1: whole rows, by one workgroup each in parts of len.

@@ -29,7 +29,13 @@ constexpr int kMaxBlocks = 1 << 20;  // workgroups of one launch; they stride ov
 // ---- 16-byte steps of a row ----------------------------------------------------------------------------------
 // A row of n elements is up to N-1 elements before the first 16-byte boundary, steps of N elements from there, and up to
 // N-1 elements behind the last step. A thread holds some steps and, where it is one of the first few, one of the single
-// elements, so that any alignment and pitch goes at full speed and nothing outside the row is touched.
+// elements, so that any alignment and pitch goes at full speed and nothing outside the row is touched. Where the
+// workgroup has places to spare, the steps are counted from the 128-byte line that the first one lies in, so that a
+// wave's 64 steps are whole lines.
+// Logits too many for the caches to keep until their reader comes (kStream bytes) are loaded and their gradient stored
+// nontemporally, but for rows that are read again in parts (LOOP): loss and gradient 16384x32000 bf16 393 -> 360 us,
+// 8192x32000 200 -> 184, the backward alone 172 -> 163, K = 20 8192x32000 116 -> 109. Followed by a reader of the gradient
+// 2048x32000 103 -> 96 us and 1000x32000 53 -> 50, but 512x32000 29.8 -> 30.5 and 8192x2000 28.7 -> 30.3.
 template <class T> struct Vec;
 template <> struct Vec<__bf16> {
   static constexpr int N = 8;
@@ -64,24 +70,42 @@ template <> struct Vec<float> {
   }
 };
 
+// keeps the compiler from making one ordinary access of a nontemporal one and its ordinary counterpart
+__device__ __forceinline__ void apart() { asm volatile(""); }
+
 template <class T> struct Steps {
-  static constexpr int N = Vec<T>::N;
-  const T* p;        // the row's first element
-  int head, steps, singles;  // elements before the steps; the steps; single elements before and behind them
-  __device__ Steps(const T* row, int n) : p(row) {
-    const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  static constexpr int N = Vec<T>::N, kLine = 128 / 16;
+  const T* p;         // the row's first element
+  int head, singles;  // single elements before the steps, and before and behind them
+  int from, steps;    // the first step's number (of those counted from its line's beginning), how many there are
+  __device__ Steps(const T* row, int n, int places) : p(row) {
+    const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>(row);
+    const int lead = (int)((at & 15) / sizeof(T));
     head = lead ? min(n, N - lead) : 0;
     steps = (n - head) / N;
     singles = n - steps * N;
+    from = (int)((at + 15) / 16 % kLine);
+    if (steps + from > places) from = 0;
   }
-  __device__ __forceinline__ int first(int v) const { return head + v * N; }  // the row's index of a step's element 0
+  __device__ __forceinline__ int end() const { return from + steps; }
+  __device__ __forceinline__ bool has(int v) const { return (unsigned)(v - from) < (unsigned)steps; }
+  __device__ __forceinline__ int origin() const { return head - from * N; }
+  __device__ __forceinline__ int first(int v) const { return origin() + v * N; }  // the row's index of a step's element 0
   __device__ __forceinline__ int single(int e) const { return e < head ? e : e + steps * N; }  // ... of single element e
   // a uniform base and an unsigned 32-bit offset: one address register a step
-  __device__ __forceinline__ u32x4 load(int v) const {
-    return *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(p + head) + (uint32_t)v * 16u);
+  __device__ __forceinline__ const u32x4* at(int v) const {
+    return reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(p + origin()) + (uint32_t)v * 16u);
   }
-  __device__ __forceinline__ void store(T* out, int v, const float* f) const {  // out: aligned like the row
-    *reinterpret_cast<u32x4*>(reinterpret_cast<char*>(out + head) + (uint32_t)v * 16u) = Vec<T>::pack(f);
+  __device__ __forceinline__ void store(T* out, int v, const float* f, bool stream) const {  // out: aligned like the row
+    u32x4* q = reinterpret_cast<u32x4*>(reinterpret_cast<char*>(out + origin()) + (uint32_t)v * 16u);
+    const u32x4 x = Vec<T>::pack(f);
+    if (stream) {
+      apart();
+      __builtin_nontemporal_store(x, q);
+      apart();
+    } else {
+      *q = x;
+    }
   }
 };
 
@@ -185,13 +209,19 @@ __device__ __forceinline__ int lane_id() {
 template <class T, int NT, int VPT> struct Held {
   u32x4 d[VPT];  // step threadIdx.x + i NT; -inf where there is none
   float x;       // single element threadIdx.x; -inf where there is none
-  __device__ __forceinline__ void load(const Steps<T>& s) {
+  __device__ __forceinline__ void load(const Steps<T>& s, bool stream) {  // stream: uniform
     const int tid = lane_id();
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = tid + i * NT;
-      d[i][0] = d[i][1] = d[i][2] = d[i][3] = Vec<T>::kNone;
-      if (v < s.steps) d[i] = s.load(v);
+    for (int i = 0; i < VPT; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = Vec<T>::kNone;
+    if (stream) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (s.has(tid + i * NT)) d[i] = __builtin_nontemporal_load(s.at(tid + i * NT));
+      apart();
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (s.has(tid + i * NT)) d[i] = *s.at(tid + i * NT);
     }
     x = (int)threadIdx.x < s.singles ? (float)s.p[s.single(threadIdx.x)] : -INFINITY;
   }
@@ -203,7 +233,7 @@ template <class T, int NT, int VPT> struct Held {
   }
   // Where step i and all behind it are nobody's: a pass ends there (uniform; looked at a quarter of the steps at a time)
   static __device__ __forceinline__ bool done(const Steps<T>& s, int i) {
-    return VPT >= 4 && i > 0 && i % (VPT / 4) == 0 && i * NT >= s.steps;
+    return VPT >= 4 && i > 0 && i % (VPT / 4) == 0 && i * NT >= s.end();
   }
   __device__ __forceinline__ float max(const Steps<T>& s) const {
     float m = x;
@@ -306,7 +336,7 @@ __device__ void best_of(const Held<T, NT, VPT>& h, const Steps<T>& s, int base, 
           const int w = u % (S::kSlots * G), i = u / (S::kSlots * G);
           if (w >= ns) continue;
           const int v = sh.first[w] + i * NT;
-          if (v >= s.steps) continue;
+          if (!s.has(v)) continue;
           const u32x4 d = sh.held[i][w];
 #pragma unroll
           for (int k = 0; k < N; ++k) take(Vec<T>::get(d, k), s.first(v) + k);
@@ -457,9 +487,9 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
     const int seg = sp.nseg == 1 ? 0 : (int)(w - row * sp.nseg);
     const T* z = (const T*)a.z + row * a.ld;
     int base = seg * sp.len, n = min(sp.len, a.V - base);
-    Steps<T> s(z + base, n);
+    Steps<T> s(z + base, n, NT * VPT);
     Held<T, NT, VPT> h;
-    h.load(s);
+    h.load(s, !LOOP && a.stream);
     const int id = sp.nseg == 1 ? token_of(a, row) : -1;
     const float z_id = id >= 0 ? (float)z[id] : 0.f;  // before the gradient may overwrite it
     const float c = a.s * kLog2e;
@@ -508,8 +538,8 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
       before_m = m; before_Z = Z; before_S = S;
       base = part * sp.len;
       n = min(sp.len, a.V - base);
-      s = Steps<T>(z + base, n);
-      h.load(s);
+      s = Steps<T>(z + base, n, NT * VPT);
+      h.load(s, !LOOP && a.stream);
     }
     const RowStat r(m, Z, S);
     float* out = sp.nseg > 1 ? sp.part + w * sp.stride : nullptr;
@@ -543,14 +573,14 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
           const int v = t0 + i * NT;
           float f[Vec<T>::N];
           g.template step<T>(h.d[i], s.first(v), f);
-          if (v < s.steps) s.store(dz + (LOOP ? base : 0), v, f);
+          if (s.has(v)) s.store(dz + (LOOP ? base : 0), v, f, a.stream);
         }
         if (tid < s.singles) dz[s.single(tid) + (LOOP ? base : 0)] = (T)g.one(h.x, s.single(tid));
         if (!LOOP || --part < 0) break;
         base = part * sp.len;
         if (id >= 0) g.id = id - base;
-        s = Steps<T>(z + base, min(sp.len, a.V - base));
-        h.load(s);
+        s = Steps<T>(z + base, min(sp.len, a.V - base), NT * VPT);
+        h.load(s, !LOOP && a.stream);
       }
     }
     __syncthreads();  // the next row's shared values
@@ -776,11 +806,11 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
     const int seg = sp.nseg == 1 ? 0 : (int)(w - row * sp.nseg);
     const T* z = (const T*)a.z + row * a.ld;
     int base = seg * sp.len, n = min(sp.len, a.V - base);
-    Steps<T> s(z + base, n);
+    Steps<T> s(z + base, n, NT * VPT);
     ListRaw raw;
     if (wave == 0) raw = fetch_list(a, row);
     Held<T, NT, VPT> h;
-    h.load(s);
+    h.load(s, !LOOP && a.stream);
     if (wave == 0) {
       if (sp.nseg == 1) {
         teach<T>(L, a, z, raw);
@@ -800,9 +830,9 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
         for (int k = lane; k < a.K; k += 64) {
           const int j = L.id[k] - base;
           if (L.id[k] < 0 || j < 0 || j >= n) continue;
-          const int at = j - s.head, v = at / Vec<T>::N;
-          const bool step = at >= 0 && v < s.steps;
-          const uint32_t b = 1u << (step ? v % 4 * 8 + at % Vec<T>::N : at < 0 ? j : j - s.steps * Vec<T>::N);
+          const int at = j - s.origin(), v = at / Vec<T>::N;
+          const bool step = j >= s.head && s.has(v);
+          const uint32_t b = 1u << (step ? v % 4 * 8 + at % Vec<T>::N : j < s.head ? j : j - s.steps * Vec<T>::N);
           twice |= (atomicOr(&bits[step ? v / 4 : NT * VPT / 4], b) & b) != 0;
         }
         if (__any(twice) && lane == 0) L.repeated = 1;
@@ -850,8 +880,8 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
       before_m = mt; before_Z = Z;
       base = part * sp.len;
       n = min(sp.len, a.V - base);
-      s = Steps<T>(z + base, n);
-      h.load(s);
+      s = Steps<T>(z + base, n, NT * VPT);
+      h.load(s, !LOOP && a.stream);
     }
     const float ref = mt == -INFINITY ? 0.f : mt;
     if (sp.nseg > 1) {
@@ -888,13 +918,13 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
           float f[Vec<T>::N];
 #pragma unroll
           for (int k = 0; k < Vec<T>::N; ++k) f[k] = zero ? 0.f : C * exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
-          if (v < s.steps) s.store(dz + (LOOP ? base : 0), v, f);
+          if (s.has(v)) s.store(dz + (LOOP ? base : 0), v, f, a.stream);
         }
         if (tid < s.singles) dz[s.single(tid) + (LOOP ? base : 0)] = (T)(zero ? 0.f : C * exp2_fast((h.x - ref) * c));
         if (!LOOP || --part < 0) break;
         base = part * sp.len;
-        s = Steps<T>(z + base, min(sp.len, a.V - base));
-        h.load(s);
+        s = Steps<T>(z + base, min(sp.len, a.V - base), NT * VPT);
+        h.load(s, !LOOP && a.stream);
       }
       __syncthreads();  // the listed tokens' own, over what the steps wrote there
       if (wave == 0)
@@ -928,12 +958,16 @@ template <class T> __global__ __launch_bounds__(64) void k_distill_join(const To
 }
 
 // ---- the gradients after the forward -----------------------------------------------------------------------------
-constexpr int kGradThreads = 256, kGradSteps = 4;  // 16 KB of a row a workgroup
+// A workgroup of the log-probabilities' gradient takes 8 KB of a row, less the places that aligning its steps may need
+// (2 steps a thread: 8192x32000 bf16 172 us; 4: 191; 8: 190; 1: 245), one of the distillation's, which reads the row's
+// list first, 16 KB at a time (4 steps: 100x131071 f32 59 us; 2: 69).
+constexpr int kGradThreads = 256, kGradSteps = 2, kTileSteps = 4;
+constexpr int grad_steps(int steps) { return kGradThreads * steps - 7; }
 
 // step v of the results at `out`, which need not be aligned like the logits
-template <class T> __device__ __forceinline__ void put_step(const Steps<T>& s, T* out, bool wide, int v, const float* f) {
+template <class T> __device__ __forceinline__ void put_step(const Steps<T>& s, T* out, bool wide, int v, const float* f, bool stream) {
   if (wide) {
-    s.store(out, v, f);
+    s.store(out, v, f, stream);
   } else {
 #pragma unroll
     for (int k = 0; k < Vec<T>::N; ++k) out[s.first(v) + k] = (T)f[k];
@@ -949,7 +983,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_bwd(const TokenArgs a
     const T* z = (const T*)a.z + row * a.ld;
     T* dz = (T*)a.dz + row * a.ldd;
     const int n = min(len, a.V - base);
-    const Steps<T> s(z + base, n);
+    const Steps<T> s(z + base, n, kGradThreads * kGradSteps);
     Held<T, kGradThreads, kGradSteps> h;
     const float* q = a.stats + row * 4;
     RowGrad g(a, row, token_of(a, row), q[0], q[1], q[2]);
@@ -959,7 +993,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_bwd(const TokenArgs a
       for (int i = 0; i < kGradSteps; ++i) h.d[i] = u32x4{0, 0, 0, 0};
       h.x = 0.f;
     } else {
-      h.load(s);
+      h.load(s, a.stream);
     }
     const bool wide = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     dz += base;
@@ -968,7 +1002,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_bwd(const TokenArgs a
       const int v = threadIdx.x + i * kGradThreads;
       float f[Vec<T>::N];
       g.template step<T>(h.d[i], s.first(v), f);
-      if (v < s.steps) put_step(s, dz, wide, v, f);
+      if (s.has(v)) put_step(s, dz, wide, v, f, a.stream);
     }
     if ((int)threadIdx.x < s.singles) dz[s.single(threadIdx.x)] = (T)g.one(h.x, s.single(threadIdx.x));
   }
@@ -986,9 +1020,9 @@ __global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a,
     T* dz = (T*)a.dz + row * a.ldd;
     const float* q = a.stats + row * 4;
     const float ref = q[2] == -INFINITY ? 0.f : q[2], c = a.s * kLog2e;
-    constexpr int kTile = kGradThreads * kGradSteps * Vec<T>::N;
-    Held<T, kGradThreads, kGradSteps> h, next;
-    h.load(Steps<T>(z + base, min(kTile, end)));
+    constexpr int kPlaces = kGradThreads * kTileSteps, kTile = grad_steps(kTileSteps) * Vec<T>::N;
+    Held<T, kGradThreads, kTileSteps> h, next;
+    h.load(Steps<T>(z + base, min(kTile, end), kPlaces), a.stream);
     // the listed logits are read here, before this workgroup's steps may overwrite them in place; another workgroup
     // may have overwritten those outside this chunk, which are not used
     if (wave == 0) {
@@ -1005,16 +1039,16 @@ __global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a,
     const float C = L.C;
     const bool zero = L.scale == 0.f;
     for (int b = 0; b < end; b += kTile, h = next) {
-      const Steps<T> s(z + base + b, min(kTile, end - b));
-      if (b + kTile < end) next.load(Steps<T>(z + base + b + kTile, min(kTile, end - b - kTile)));
+      const Steps<T> s(z + base + b, min(kTile, end - b), kPlaces);
+      if (b + kTile < end) next.load(Steps<T>(z + base + b + kTile, min(kTile, end - b - kTile), kPlaces), a.stream);
       T* out = dz + base + b;
 #pragma unroll
-      for (int i = 0; i < kGradSteps; ++i) {
+      for (int i = 0; i < kTileSteps; ++i) {
         const int v = threadIdx.x + i * kGradThreads;
         float f[Vec<T>::N];
 #pragma unroll
         for (int k = 0; k < Vec<T>::N; ++k) f[k] = zero ? 0.f : C * exp2_fast((Vec<T>::get(h.d[i], k) - ref) * c);
-        if (v < s.steps) put_step(s, out, wide, v, f);
+        if (s.has(v)) put_step(s, out, wide, v, f, a.stream);
       }
       if ((int)threadIdx.x < s.singles) out[s.single(threadIdx.x)] = (T)(zero ? 0.f : C * exp2_fast((h.x - ref) * c));
     }
@@ -1027,6 +1061,7 @@ __global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a,
 }
 
 // ---- launches ----------------------------------------------------------------------------------------------------
+constexpr int kCUs = 256;
 constexpr int kHeld = 1024 * 16;    // steps that the largest workgroup holds
 // Rows from which on long ones go whole, in parts, to one workgroup (a CU) each. It reads them once instead of twice, but
 // loads little ahead and fills the CUs in whole rounds: f32 V = 131071 on 256 CUs, whole against segments and a gradient
@@ -1037,9 +1072,12 @@ constexpr int kSegment = 256 * 16;  // ... and that the largest of 256 threads h
 
 // How rows of V elements are split over workgroups of `held` steps (a row of at most N-1 elements more than a workgroup's
 // steps goes with those as its single elements, however it is aligned). With its gradient a row stays whole where it can,
-// to be read once (and wherever the gradient is written, so that it is the same), and a longer one whole in parts where
-// there are rows enough to keep every CU at one of its own; without, segments keep more loads in flight.
-RowSplit split_of(int V, int dt, int K, bool grad, bool loop) {
+// to be read once (and wherever the gradient is written, so that it is the same): f32 V = 50001 whole against segments and
+// a gradient launch, T = 4 11.9 us : 18.2, 1000 97 : 119, 4095 328 : 448. A longer one stays whole in parts where there
+// are rows enough to keep every CU at one of its own. Without a gradient, segments keep more loads in flight, but need a
+// second launch, which pays off only once every CU has a row (f32 V = 50001, T = 16 K = 0 13.0 us in segments : 9.5 whole,
+// 256 15.4 : 14.1, 1000 39.8 : 51.8, 1000 K = 20 52 : 81; segments of 32 KB 50 at K = 5, of 64 KB 48).
+RowSplit split_of(int T, int V, int dt, int K, bool grad, bool loop) {
   const int n = dt == BF16 ? 8 : 4;
   RowSplit sp;
   if (loop && grad && V / n > kHeld) {
@@ -1048,7 +1086,7 @@ RowSplit split_of(int V, int dt, int K, bool grad, bool loop) {
     sp.steps = kHeld;
     return sp;
   }
-  const int held = grad && V / n <= kHeld ? kHeld : kSegment, cap = held * n;
+  const int held = V / n <= kHeld && (grad || T <= kCUs) ? kHeld : kSegment, cap = held * n;
   if (V / n > held) sp.nseg = (V + cap - 1) / cap;
   sp.len = sp.nseg == 1 ? V : ((V + sp.nseg - 1) / sp.nseg + 63) / 64 * 64;  // <= cap, and whole steps
   sp.stride = 4 + 2 * K;
@@ -1061,9 +1099,18 @@ bool same_alignment(const TokenArgs& a) {
   return ((reinterpret_cast<uintptr_t>(a.z) ^ reinterpret_cast<uintptr_t>(a.dz)) & 15) == 0 &&
          (a.T == 1 || (a.ld - a.ldd) * e % 16 == 0);
 }
+constexpr int64_t kStream = 48 << 20;
+bool streams(const TokenArgs& a) { return (int64_t)a.T * a.V * (int64_t)dtype_size(a.dt) >= kStream; }
 dim3 grid_of(int64_t n) { return dim3((unsigned)std::min<int64_t>(n, kMaxBlocks)); }
 
-// f(type, threads, steps a thread) for the smallest workgroup that holds `steps`
+// f(type, threads, steps a thread) for the smallest workgroup that holds `steps`. Measured in bf16, loss and gradient if
+// not said otherwise:
+//  - one wave a row where it holds it: 16384x1000 18.4 us, 256 threads 46.4; 16384x2048 31.4 : 51.7; 16384x4000 57.4 : 58.3;
+//    K = 32 alternatives of 16384x2000 32.8 : 68.6, but at K = 64 of its 64 threads all must hold one: 1079 : 84.8
+//  - 256 threads up to 64 KB, four rows a CU at a time: 8192x32000 200 us, 1024 threads 279; with K = 20 114 : 275;
+//    distillation 216 : 339
+//  - 1024 threads from 1024 steps on where rows are few, for the latency: 256x32000 11.7 us, 256 threads 12.5; at 512 rows
+//    21.3 : 19.1
 template <int A, int B> struct Size { static constexpr int NT = A, VPT = B; };
 template <class T, class F> void by_size(int steps, int64_t groups, int K, F f) {
   const bool few = groups < 512;
@@ -1086,15 +1133,16 @@ template <class F> hipError_t by_type(int dt, F f) {
 }  // namespace
 
 size_t logprobs_part_bytes(int T, int V, int dt, int K) {
-  const RowSplit sp = split_of(V, dt, K, false, false);
+  const RowSplit sp = split_of(T, V, dt, K, false, false);
   return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
 
 hipError_t launch_logprobs(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  RowSplit sp = split_of(a.V, a.dt, a.K, args.dz, a.K == 0 && a.T >= kLoopLogprobs);
+  RowSplit sp = split_of(a.T, a.V, a.dt, a.K, args.dz, a.K == 0 && a.T >= kLoopLogprobs);
   const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in its own launch
   sp.part = part;
+  a.stream = streams(a);
   if (after) a.dz = nullptr;
   {
     const double e = dtype_size(a.dt), n = (double)a.T * a.V;
@@ -1122,8 +1170,10 @@ hipError_t launch_logprobs(const TokenArgs& args, float* part, hipStream_t st) {
   return e != hipSuccess || !after ? e : launch_logprobs_bwd(args, st);
 }
 
-hipError_t launch_logprobs_bwd(const TokenArgs& a, hipStream_t st) {
-  const int n = a.dt == BF16 ? 8 : 4, len = kGradThreads * kGradSteps * n, chunks = (a.V + len - 1) / len;
+hipError_t launch_logprobs_bwd(const TokenArgs& args, hipStream_t st) {
+  TokenArgs a = args;
+  a.stream = streams(a);
+  const int n = a.dt == BF16 ? 8 : 4, len = grad_steps(kGradSteps) * n, chunks = (a.V + len - 1) / len;
   ProfScope prof(POET_K_HEAD, st, 6.0 * a.T * a.V, 2.0 * a.T * a.V * dtype_size(a.dt));
   return by_type(a.dt, [&](auto t) {
     hipLaunchKernelGGL(k_logprobs_bwd<decltype(t)>, grid_of((int64_t)a.T * chunks), dim3(kGradThreads), 0, st, a, chunks, len);
@@ -1131,15 +1181,16 @@ hipError_t launch_logprobs_bwd(const TokenArgs& a, hipStream_t st) {
 }
 
 size_t distill_part_bytes(int T, int V, int dt) {
-  const RowSplit sp = split_of(V, dt, 0, false, false);
+  const RowSplit sp = split_of(T, V, dt, 0, false, false);
   return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
 
 hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  RowSplit sp = split_of(a.V, a.dt, 0, args.dz, a.T >= kLoopDistill);
+  RowSplit sp = split_of(a.T, a.V, a.dt, 0, args.dz, a.T >= kLoopDistill);
   const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in its own launch
   sp.part = part;
+  a.stream = streams(a);
   if (after) a.dz = nullptr;
   {
     const double e = dtype_size(a.dt), n = (double)a.T * a.V;
@@ -1165,9 +1216,11 @@ hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
   return e != hipSuccess || !after ? e : launch_distill_bwd(args, st);
 }
 
-hipError_t launch_distill_bwd(const TokenArgs& a, hipStream_t st) {
+hipError_t launch_distill_bwd(const TokenArgs& args, hipStream_t st) {
+  TokenArgs a = args;
+  a.stream = streams(a);
   // a workgroup reads its row's list once for several tiles, while there are workgroups enough
-  const int tile = kGradThreads * kGradSteps * (a.dt == BF16 ? 8 : 4);
+  const int tile = grad_steps(kTileSteps) * (a.dt == BF16 ? 8 : 4);
   const int64_t tiles = (a.V + tile - 1) / tile;
   const int len = tile * (int)std::min<int64_t>(16, std::max<int64_t>(1, tiles * a.T / 4096));
   const int chunks = (a.V + len - 1) / len;

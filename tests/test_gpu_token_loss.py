@@ -405,6 +405,53 @@ def test_long_rows_whole(V, dt, pad):
     assert torch.equal(zt, apart)
 
 
+@pytest.mark.parametrize("dt,V", [("bf16", v) for v in (504, 1000, 1024, 2040, 4096, 8192, 16376, 32744, 32768)] +
+                         [("f32", v) for v in (255, 512, 2047, 4096, 8180, 16384)])
+def test_rows_that_fill_a_workgroup(dt, V):
+    """Rows of as many 16-byte steps as a workgroup has places, or a few less, at every place in a line of memory: those
+    that have room start at a line's beginning, the others do not."""
+    T, K = 520, 9
+    announce(f"rows that fill a workgroup V={V} {dt}")
+    rng = np.random.default_rng(V)
+    pad = {"bf16": 8, "f32": 4}[dt] if V % 8 == 0 else 1  # the next row starts one step later, or anywhere
+    zt, z, _ = rows(gauss(T, V, 18), dt, pad, skew=pad)
+    ids = rng.integers(-1, V, T)
+    ids[:4] = [0, 1, V - 1, V - 2]
+    check_logprobs(zt, z, ids, K=K, gl=rng.standard_normal(T), gh=rng.standard_normal(T), dt=dt,
+                   dz=torch.empty((T, V + pad), dtype=zt.dtype, device="cuda")[:, :V])
+    t_ids, t_z, _ = teacher(z, K, V)
+    t_ids[:, :2] = [0, V - 1]
+    check_distill(zt, z, t_ids, t_z, tail=bool(V & 8), w=rng.standard_normal(T), dt=dt)
+
+
+@pytest.mark.parametrize("V,dt,pad", [(16411, "f32", 0), (40001, "f32", 3), (33333, "bf16", 1), (65536, "bf16", 8)])
+def test_rows_in_segments(V, dt, pad):
+    """Rows of 64 to 256 KB without a gradient, more of them than fit a workgroup each: masks that empty a segment or all
+    of a row, equal logits across segments, a NaN; the same numbers as for the rows one at a time, to the bounds."""
+    T, K = 260, 40
+    announce(f"rows in segments V={V} {dt}")
+    rng = np.random.default_rng(V)
+    z = gauss(T, V, 19)
+    z[0, : V // 2 + 100] = -INF
+    z[1, V // 2 - 100:] = -INF
+    z[2] = -INF
+    z[3, 5:] = -INF
+    z[4], z[5] = np.round(z[4]), 1.5
+    z[6, V - 3] = float("nan")
+    zt, z, _ = rows(z, dt, pad)
+    ids = rng.integers(-1, V, T)
+    check_logprobs(zt, z, ids, s=1.3, K=K, dt=dt)
+    few = slice(0, 9)
+    check_logprobs(zt[few], z[few], ids[few], s=1.3, K=K, dt=dt)
+    t_ids, t_z, lse = teacher(np.where(np.isfinite(z), z, -50.0), K, V)
+    t_ids[9, 4:9] = t_ids[9, 0]
+    t_ids[10] = -1
+    for tail in (False, True):
+        lt = lse + 0.2 if tail else None
+        check_distill(zt, z, t_ids, t_z, tail=tail, lse=lt, dt=dt)
+        check_distill(zt[few], z[few], t_ids[few], t_z[few], tail=tail, lse=lt[few] if tail else None, dt=dt)
+
+
 def test_more_rows_than_workgroups():
     """More rows than one launch has workgroups."""
     T, V, P = 1_100_003, 9, 7
