@@ -8,6 +8,14 @@
 // columns each (16 bytes of bf16) in registers between the two means, and keep their columns' weights for all tokens
 // that the workgroup takes, loading the next token's columns while they work on one. In the backward a workgroup takes a
 // run of consecutive tokens and sums its weights' gradients in registers; a second launch adds the workgroups' sums.
+//
+// Reached (HBM bytes that cannot be avoided over the time; a large copy reaches 5.1-5.3 TB/s): forward 16384x2048 bf16,
+// gated per token, 63 us, 5.3 TB/s; backward 32768x2560, float32 residual, bf16 activations, a gate row for 512 tokens,
+// 300 us, 5.0 TB/s; backward 1001x1377 f32 without post norm and gate 14.8 us, of which the two kernels take 8 and 5: latency.
+// The first form, a workgroup a token that reads memory for every pass, and the weight gradients' sums by a thread a
+// column, took 206 us, 44.7 ms and 334 us. Stores past the caches (nontemporal) make the forward alone faster (4000x2048
+// bf16 15.4 -> 14.9 us, 8192x1377 31.6 -> 23.7) and what reads x and h' right after it slower by more (29.1 -> 32.7,
+// 46.8 -> 48.8 for both): not used.
 #include <algorithm>
 
 #include "../../include/poet.h"
@@ -24,7 +32,9 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 //   WIDE    the same for any d >= 8: where d is no multiple of 8 the last thread with columns reads the row's last 8 and
 //           drops those that are its neighbour's; threads past it read them too and drop all
 //   SINGLE  column g of thread g (d < 8, one element a thread)
-// EXACT and WIDE read and write 16 bytes at a time whatever the row's alignment (global accesses need none). No load is
+// EXACT saves WIDE's clamping and masking (backward 32768x2560 300 us : 312, forward 16384x2048 67.4 : 68.2).
+// EXACT and WIDE read and write 16 bytes at a time whatever the row's alignment (global accesses need none; element by
+// element where it is not 16 bytes, the forward 8192x5461 bf16 took 199 us, now 102). No load is
 // conditional: the wait for a token's loads would otherwise have to wait for the stores between them too.
 enum { EXACT = 0, WIDE = 1, SINGLE = 2 };
 // The row's address in scalar registers, for the compiler a new one each time: it would keep a 64-bit address a thread
@@ -136,7 +146,8 @@ __device__ __forceinline__ float block_sum(float v, float (*red)[16], int& turn)
 }
 
 // Which parts a call has, known to the compiler for the common ones (y, x and their gradients, and h' from past the seam,
-// all given); PARTS_ANY looks at the arguments.
+// all given); PARTS_ANY looks at the arguments (backward 32768x2560 356 us, 300 with its parts known; forward 16384x2048
+// 67.3 : 66.9).
 enum { PARTS_POST = 1, PARTS_GATE = 2, PARTS_ANY = 4 };
 
 // ---- forward --------------------------------------------------------------------------------------------------------
@@ -403,7 +414,8 @@ __global__ __launch_bounds__(MAXT, MAXT <= 512 ? 3 : 4) void k_norm_bwd(const No
 
 // Adds the chunks' sums in a fixed order, 64 columns and 16 threads a column in a workgroup. y = 0, 1: all chunks into
 // dw_pre, dw_post, every 16th chunk a thread. y >= 2: the gate rows' chunks (stored as TA), a row a workgroup the same way
-// where a row has many, else a row a thread (per_thread).
+// where a row has many, else a row a thread (per_thread): 32768x2048 with a gate row for 256 tokens, backward and sums 168
+// us so, 178 a row a workgroup; for 1024 and 4096 tokens the same, for 16384 176 : 168.
 template <class TA>
 __global__ __launch_bounds__(1024) void k_norm_sums(const NormArgs a, const NormPlan p, const float* part, int rows,
                                                     bool per_thread) {

@@ -7,6 +7,17 @@
 // workgroup keeps a whole row in registers, 16 bytes a thread and step, and every pass over it (maximum, sums, best
 // alternatives, gradient) reads those. Rows beyond a workgroup's registers are split into segments whose maxima, sums
 // and best alternatives a second launch joins; their gradient is a launch of its own.
+//
+// Reached (HBM bytes that cannot be avoided over the time; a large copy reaches 5.1-5.3 TB/s, a read alone 5.6):
+//   log p, entropy, K = 20 best, 8192x32000 bf16                109 us, 4.8 TB/s; without alternatives 83 us, 6.3 TB/s
+//   the same with K = 5, half of the vocabulary masked, 1000x50001 f32   45 us, 4.4 TB/s
+//   log p and gradient, 16384x32000 bf16                        358 us, 5.9 TB/s
+//   gradient alone, 4095x50001 f32, pitch 50008                 268 us, 6.1 TB/s
+//   distillation and gradient, K = 64, 8192x32000 bf16          205 us, 5.1 TB/s
+//   the same, K = 100, 511x131071 f32                           136 us, 3.9 TB/s (half of each row is read twice)
+//   one row of 32000 with its 20 best                            10 us: the search's chain of steps, not its bytes
+// The first form, one workgroup a row with a pass over memory for each maximum, sum and alternative, took 4242, -, 1724,
+// 394, 9645 and 3325 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -475,6 +486,9 @@ __device__ __forceinline__ void add_part(float& Z, float& S, float ref, float m0
   S += e * fmaf(Z0, fmaxf(t, kLow), S0);
 }
 
+// One pass over HBM: the entropy's sum comes with Z's from the same exponentials (two fused multiply-adds an element more),
+// and the gradient from the registers. Loading the next row behind the gradient's stores, by workgroups that stay, was
+// slower than new workgroups a row (16384x32000 403 us, 362 without): four rows a CU overlap by themselves.
 // One workgroup a row (nseg == 1: results, and the gradient where asked) or a segment of a row (partials into `part`:
 // m, Z, S, -, then the K best keys). LOOP: a row in sp.loops parts, one after another; the last one stays in the registers
 // for its gradient, the others are read again.
@@ -587,7 +601,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(const TokenArgs a, const Row
   }
 }
 
-// joins the segments of each row: one workgroup a row
+// Joins the segments of each row: one workgroup a row, about 3 us of latency. In 64 bits, because there are few.
 __global__ __launch_bounds__(256) void k_logprobs_join(const TokenArgs a, const RowSplit sp) {
   const int tid = threadIdx.x, lane = tid & 63;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
@@ -794,7 +808,9 @@ __device__ __forceinline__ float grad_listed(const List& L, int k, float s) {
   return L.scale == 0.f ? 0.f : L.scale * (exp_of(((double)L.z[k] - ref) * s - L.logZ) - L.all[k]);
 }
 
-// One workgroup a row or segment, as k_logprobs; partials: mt, Zt.
+// One workgroup a row or segment, as k_logprobs; partials: mt, Zt. The list is fetched before the row and worked on by one
+// wave while the row arrives: its chain of dependent reads and logarithms is what is left beside the bytes (8192x32000
+// with its gradient 205 us, 184 for the log-probabilities').
 template <class T, int NT, int VPT, bool LOOP>
 __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowSplit sp) {
   __shared__ List L;
@@ -974,6 +990,8 @@ template <class T> __device__ __forceinline__ void put_step(const Steps<T>& s, T
   }
 }
 
+// Every element alone, from the statistics that the forward left: read once, written once (6.1-6.4 TB/s). Last rows first:
+// after a forward over fewer logits than the caches hold the last ones are still there.
 template <class T>
 __global__ __launch_bounds__(kGradThreads) void k_logprobs_bwd(const TokenArgs a, int chunks, int len) {
   const int64_t total = (int64_t)a.T * chunks;
