@@ -990,14 +990,14 @@ template <class T> __device__ __forceinline__ void put_step(const Steps<T>& s, T
   }
 }
 
-// Every element alone, from the statistics that the forward left: read once, written once (6.1-6.4 TB/s). Last rows first:
-// after a forward over fewer logits than the caches hold the last ones are still there.
+// Every element alone, from the statistics that the forward left: read once, written once (6.1-6.4 TB/s). The rows' order
+// does not matter: last ones first, after a forward over what the caches can hold, 1000x32000 41.8 us for both, 42.2 in order.
 template <class T>
 __global__ __launch_bounds__(kGradThreads) void k_logprobs_bwd(const TokenArgs a, int chunks, int len) {
   const int64_t total = (int64_t)a.T * chunks;
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
-    const int64_t at = total - 1 - w, row = at / chunks;  // last rows first: they are the nearest in the caches
-    const int base = (int)(at - row * chunks) * len;
+    const int64_t row = w / chunks;
+    const int base = (int)(w - row * chunks) * len;
     const T* z = (const T*)a.z + row * a.ld;
     T* dz = (T*)a.dz + row * a.ldd;
     const int n = min(len, a.V - base);
@@ -1032,8 +1032,8 @@ __global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a,
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t total = (int64_t)a.T * chunks;
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
-    const int64_t at = total - 1 - w, row = at / chunks;  // last rows first: they are the nearest in the caches
-    const int base = (int)(at - row * chunks) * len, end = min(len, a.V - base);
+    const int64_t row = w / chunks;
+    const int base = (int)(w - row * chunks) * len, end = min(len, a.V - base);
     const T* z = (const T*)a.z + row * a.ld;
     T* dz = (T*)a.dz + row * a.ldd;
     const float* q = a.stats + row * 4;
@@ -1080,6 +1080,7 @@ __global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a,
 
 // ---- launches ----------------------------------------------------------------------------------------------------
 constexpr int kCUs = 256;
+constexpr int kWholeLogprobs = 1024 * 13;  // 208 KB
 constexpr int kHeld = 1024 * 16;    // steps that the largest workgroup holds
 // Rows from which on long ones go whole, in parts, to one workgroup (a CU) each. It reads them once instead of twice, but
 // loads little ahead and fills the CUs in whole rounds: f32 V = 131071 on 256 CUs, whole against segments and a gradient
@@ -1093,9 +1094,11 @@ constexpr int kSegment = 256 * 16;  // ... and that the largest of 256 threads h
 // to be read once (and wherever the gradient is written, so that it is the same): f32 V = 50001 whole against segments and
 // a gradient launch, T = 4 11.9 us : 18.2, 1000 97 : 119, 4095 328 : 448. A longer one stays whole in parts where there
 // are rows enough to keep every CU at one of its own. Without a gradient, segments keep more loads in flight, but need a
-// second launch, which pays off only once every CU has a row (f32 V = 50001, T = 16 K = 0 13.0 us in segments : 9.5 whole,
-// 256 15.4 : 14.1, 1000 39.8 : 51.8, 1000 K = 20 52 : 81; segments of 32 KB 50 at K = 5, of 64 KB 48).
-RowSplit split_of(int T, int V, int dt, int K, bool grad, bool loop) {
+// second launch: while no CU has two rows, rows up to `whole` steps stay whole (f32 V = 50001, 200 KB, K = 0, T = 16 in
+// segments 13.0 us as called, 6.9 in a graph : whole 9.5 and 7.5; 256 15.4 : 14.1 as called; 1000 39.8 : 51.8, K = 20 52 :
+// 81). Of 256 KB, bf16 V = 131072, T = 1 7.5 us in a graph : 12.2, K = 20 14.0 : 18.5, distillation 11.9 : 13.4, T = 256 23.7 : 21.0.
+// Segments are of 64 KB: 1000x50001 48 us at K = 5, of 32 KB 50.
+RowSplit split_of(int T, int V, int dt, int K, bool grad, bool loop, int whole) {
   const int n = dt == BF16 ? 8 : 4;
   RowSplit sp;
   if (loop && grad && V / n > kHeld) {
@@ -1104,7 +1107,7 @@ RowSplit split_of(int T, int V, int dt, int K, bool grad, bool loop) {
     sp.steps = kHeld;
     return sp;
   }
-  const int held = V / n <= kHeld && (grad || T <= kCUs) ? kHeld : kSegment, cap = held * n;
+  const int held = V / n <= (grad ? kHeld : T <= kCUs ? whole : 0) ? kHeld : kSegment, cap = held * n;
   if (V / n > held) sp.nseg = (V + cap - 1) / cap;
   sp.len = sp.nseg == 1 ? V : ((V + sp.nseg - 1) / sp.nseg + 63) / 64 * 64;  // <= cap, and whole steps
   sp.stride = 4 + 2 * K;
@@ -1151,13 +1154,13 @@ template <class F> hipError_t by_type(int dt, F f) {
 }  // namespace
 
 size_t logprobs_part_bytes(int T, int V, int dt, int K) {
-  const RowSplit sp = split_of(T, V, dt, K, false, false);
+  const RowSplit sp = split_of(T, V, dt, K, false, false, kWholeLogprobs);
   return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
 
 hipError_t launch_logprobs(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  RowSplit sp = split_of(a.T, a.V, a.dt, a.K, args.dz, a.K == 0 && a.T >= kLoopLogprobs);
+  RowSplit sp = split_of(a.T, a.V, a.dt, a.K, args.dz, a.K == 0 && a.T >= kLoopLogprobs, kWholeLogprobs);
   const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in its own launch
   sp.part = part;
   a.stream = streams(a);
@@ -1199,13 +1202,13 @@ hipError_t launch_logprobs_bwd(const TokenArgs& args, hipStream_t st) {
 }
 
 size_t distill_part_bytes(int T, int V, int dt) {
-  const RowSplit sp = split_of(T, V, dt, 0, false, false);
+  const RowSplit sp = split_of(T, V, dt, 0, false, false, kHeld);
   return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
 
 hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  RowSplit sp = split_of(a.T, a.V, a.dt, 0, args.dz, a.T >= kLoopDistill);
+  RowSplit sp = split_of(a.T, a.V, a.dt, 0, args.dz, a.T >= kLoopDistill, kHeld);
   const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in its own launch
   sp.part = part;
   a.stream = streams(a);
