@@ -317,7 +317,8 @@ struct TokenArgs {
 };
 // Rows in nseg segments of len elements (1: whole rows): segment q of row t leaves its partials at part + (t nseg + q)
 // stride floats; a segment is `steps` 16-byte steps at most. loops > 1: whole rows, by one workgroup each in parts of len.
-struct RowSplit { int nseg = 1, len = 0, stride = 0, steps = 0, loops = 1; float* part = nullptr; };
+// ready (distillation's gradient after its segments): a record of each row that the join leaves for the gradient's launch.
+struct RowSplit { int nseg = 1, len = 0, stride = 0, steps = 0, loops = 1; float* part = nullptr; float* ready = nullptr; };
 // scratch of the launches below (0 where a workgroup holds a row, however it is aligned)
 size_t logprobs_part_bytes(int T, int V, int dt, int K);
 size_t distill_part_bytes(int T, int V, int dt);

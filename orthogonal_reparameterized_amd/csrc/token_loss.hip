@@ -951,6 +951,10 @@ __global__ __launch_bounds__(NT, 4) void k_distill(const TokenArgs a, const RowS
   }
 }
 
+// A row's record for k_distill_apply: the unlisted tokens' factor C, their maximum, 0 where the row's gradient is 0, -; the
+// listed tokens, -1 where an entry does not stand for one; their gradients.
+constexpr int kReadyIds = 4, kReady = kReadyIds + 2 * POET_MAX_TOP;
+
 template <class T> __global__ __launch_bounds__(64) void k_distill_join(const TokenArgs a, const RowSplit sp) {
   __shared__ List L;
   const int lane = threadIdx.x;
@@ -969,6 +973,16 @@ template <class T> __global__ __launch_bounds__(64) void k_distill_join(const To
       Zt += (double)p[1] * exp2f((p[0] == -INFINITY ? 0.f : p[0] - (mt == -INFINITY ? 0.f : mt)) * a.s * kLog2e);
     }
     finish_distill(L, a, row, mt, wave_sum(Zt));
+    if (sp.ready) {
+      if (lane == 0) grad_factors(L, a);
+      wave_fence();
+      float* r = sp.ready + row * kReady;
+      if (lane == 0) { r[0] = L.C; r[1] = mt; r[2] = L.scale == 0.f ? 0.f : 1.f; }
+      for (int k = lane; k < a.K; k += 64) {
+        reinterpret_cast<int*>(r + kReadyIds)[k] = stands(L, k) ? L.id[k] : -1;
+        r[kReadyIds + POET_MAX_TOP + k] = stands(L, k) ? grad_listed(L, k, a.s) : 0.f;
+      }
+    }
     __syncthreads();
   }
 }
@@ -1023,6 +1037,42 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_bwd(const TokenArgs a
       if (s.has(v)) put_step(s, dz, wide, v, f, a.stream);
     }
     if ((int)threadIdx.x < s.singles) dz[s.single(threadIdx.x)] = (T)g.one(h.x, s.single(threadIdx.x));
+  }
+}
+
+// The gradient of rows that went in segments, from what their join left: the list's chain of logarithms is not repeated by
+// each of a row's workgroups (100x131071 f32, K = 100: 44 us, with
+// k_distill_bwd in its place 59).
+template <class T>
+__global__ __launch_bounds__(kGradThreads) void k_distill_apply(const TokenArgs a, const RowSplit sp, int chunks, int len) {
+  const int64_t total = (int64_t)a.T * chunks;
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    const int64_t row = w / chunks;
+    const int base = (int)(w - row * chunks) * len, n = min(len, a.V - base);
+    const T* z = (const T*)a.z + row * a.ld;
+    T* dz = (T*)a.dz + row * a.ldd;
+    const float* r = sp.ready + row * kReady;
+    const Steps<T> s(z + base, n, kGradThreads * kGradSteps);
+    Held<T, kGradThreads, kGradSteps> h;
+    h.load(s, a.stream);
+    const int k = threadIdx.x;  // K <= POET_MAX_TOP <= kGradThreads
+    const int at = k < a.K ? reinterpret_cast<const int*>(r + kReadyIds)[k] - base : -1;
+    const float listed = k < a.K ? r[kReadyIds + POET_MAX_TOP + k] : 0.f;
+    const float C = r[0], ref = r[1] == -INFINITY ? 0.f : r[1], c = a.s * kLog2e;
+    const bool zero = r[2] == 0.f;
+    const bool wide = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+    dz += base;
+#pragma unroll
+    for (int i = 0; i < kGradSteps; ++i) {
+      const int v = threadIdx.x + i * kGradThreads;
+      float f[Vec<T>::N];
+#pragma unroll
+      for (int q = 0; q < Vec<T>::N; ++q) f[q] = zero ? 0.f : C * exp2_fast((Vec<T>::get(h.d[i], q) - ref) * c);
+      if (s.has(v)) put_step(s, dz, wide, v, f, a.stream);
+    }
+    if ((int)threadIdx.x < s.singles) dz[s.single(threadIdx.x)] = (T)(zero ? 0.f : C * exp2_fast((h.x - ref) * c));
+    __syncthreads();  // the listed tokens' own, over what the steps wrote there
+    if (at >= 0 && at < n) dz[at] = (T)listed;
   }
 }
 
@@ -1082,11 +1132,16 @@ __global__ __launch_bounds__(kGradThreads) void k_distill_bwd(const TokenArgs a,
 constexpr int kCUs = 256;
 constexpr int kWholeLogprobs = 1024 * 13;  // 208 KB
 constexpr int kHeld = 1024 * 16;    // steps that the largest workgroup holds
-// Rows from which on long ones go whole, in parts, to one workgroup (a CU) each. It reads them once instead of twice, but
-// loads little ahead and fills the CUs in whole rounds: f32 V = 131071 on 256 CUs, whole against segments and a gradient
-// launch, which read the distillation's list again too: distillation T = 211 70 us : 106, 511 150 : 189, 2048 515 : 654;
-// log-probabilities T = 300 107 : 97, 600 178 : 180, 1000 268 : 286, 2048 517 : 581.
-constexpr int kLoopLogprobs = 512, kLoopDistill = 200;
+// Whether rows that no workgroup holds go whole, in parts, to one workgroup (a CU) each where they have a gradient. It reads
+// them once and a part less, instead of twice, but fills the CUs in whole rounds. f32 V = 131071, whole : segments and a
+// gradient launch, distillation T = 100 35.5 us : 44.4, 150 45 : 56, 256 75 : 83, 300 101 : 94, 400 112 : 118, 512 135 :
+// 146, 600 167 : 168, 1000 253 : 268; log-probabilities T = 100 33.8 : 34.7, 256 66 : 71, 300 95 : 81, 400 105 : 104, 512 126 :
+// 132, 600 162 : 152, 1000 249 : 249, 2000 446 : 496; bf16 V = 200000, distillation T = 100 45 : 37, 200 52 : 61.
+bool whole_in_parts(int T) {
+  const int64_t rounds = ((int64_t)T + kCUs - 1) / kCUs;
+  return T >= kCUs / 2 && (rounds == 1 || 4 * (int64_t)T >= 3 * kCUs * rounds);
+}
+constexpr int kSomeApart = 3 * kCUs;  // from so many rows on always
 constexpr int kSegment = 256 * 16;  // ... and that the largest of 256 threads holds, four of which share a CU
 
 // How rows of V elements are split over workgroups of `held` steps (a row of at most N-1 elements more than a workgroup's
@@ -1098,10 +1153,10 @@ constexpr int kSegment = 256 * 16;  // ... and that the largest of 256 threads h
 // segments 13.0 us as called, 6.9 in a graph : whole 9.5 and 7.5; 256 15.4 : 14.1 as called; 1000 39.8 : 51.8, K = 20 52 :
 // 81). Of 256 KB, bf16 V = 131072, T = 1 7.5 us in a graph : 12.2, K = 20 14.0 : 18.5, distillation 11.9 : 13.4, T = 256 23.7 : 21.0.
 // Segments are of 64 KB: 1000x50001 48 us at K = 5, of 32 KB 50.
-RowSplit split_of(int T, int V, int dt, int K, bool grad, bool loop, int whole) {
+RowSplit split_of(int T, int V, int dt, int K, bool grad, int whole) {
   const int n = dt == BF16 ? 8 : 4;
   RowSplit sp;
-  if (loop && grad && V / n > kHeld) {
+  if (grad && K == 0 && V / n > kHeld && whole_in_parts(T)) {
     sp.loops = (V + kHeld * n - 1) / (kHeld * n);
     sp.len = ((V + sp.loops - 1) / sp.loops + 63) / 64 * 64;
     sp.steps = kHeld;
@@ -1154,13 +1209,13 @@ template <class F> hipError_t by_type(int dt, F f) {
 }  // namespace
 
 size_t logprobs_part_bytes(int T, int V, int dt, int K) {
-  const RowSplit sp = split_of(T, V, dt, K, false, false, kWholeLogprobs);
+  const RowSplit sp = split_of(T, V, dt, K, false, kWholeLogprobs);
   return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
 }
 
 hipError_t launch_logprobs(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  RowSplit sp = split_of(a.T, a.V, a.dt, a.K, args.dz, a.K == 0 && a.T >= kLoopLogprobs, kWholeLogprobs);
+  RowSplit sp = split_of(a.T, a.V, a.dt, a.K, args.dz, kWholeLogprobs);
   const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in its own launch
   sp.part = part;
   a.stream = streams(a);
@@ -1202,16 +1257,19 @@ hipError_t launch_logprobs_bwd(const TokenArgs& args, hipStream_t st) {
 }
 
 size_t distill_part_bytes(int T, int V, int dt) {
-  const RowSplit sp = split_of(T, V, dt, 0, false, false, kHeld);
-  return sp.nseg == 1 ? 0 : (size_t)T * sp.nseg * sp.stride * 4;
+  const RowSplit sp = split_of(T, V, dt, 0, false, kHeld);
+  if (sp.nseg == 1) return 0;
+  const bool ready = V / (dt == BF16 ? 8 : 4) > kHeld;  // with a gradient in segments too, for some numbers of rows
+  return ((size_t)T * sp.nseg * sp.stride + (ready ? (size_t)std::min(T, kSomeApart) * kReady : 0)) * 4;
 }
 
 hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
   TokenArgs a = args;
-  RowSplit sp = split_of(a.T, a.V, a.dt, 0, args.dz, a.T >= kLoopDistill, kHeld);
+  RowSplit sp = split_of(a.T, a.V, a.dt, 0, args.dz, kHeld);
   const bool after = a.dz && (sp.nseg > 1 || !same_alignment(a));  // the gradient in its own launch
   sp.part = part;
   a.stream = streams(a);
+  if (after && sp.nseg > 1) sp.ready = part + (size_t)a.T * sp.nseg * sp.stride;
   if (after) a.dz = nullptr;
   {
     const double e = dtype_size(a.dt), n = (double)a.T * a.V;
@@ -1234,13 +1292,21 @@ hipError_t launch_distill(const TokenArgs& args, float* part, hipStream_t st) {
     ProfScope prof(POET_K_HEAD, st, 0, (double)a.T * sp.nseg * sp.stride * 4);
     e = by_type(a.dt, [&](auto t) { hipLaunchKernelGGL(k_distill_join<decltype(t)>, grid_of(a.T), dim3(64), 0, st, a, sp); });
   }
-  return e != hipSuccess || !after ? e : launch_distill_bwd(args, st);
+  if (e != hipSuccess || !after) return e;
+  if (!sp.ready) return launch_distill_bwd(args, st);
+  a.dz = args.dz;
+  const int len = grad_steps(kGradSteps) * (a.dt == BF16 ? 8 : 4), chunks = (a.V + len - 1) / len;
+  ProfScope prof(POET_K_HEAD, st, 4.0 * a.T * a.V, 2.0 * a.T * a.V * dtype_size(a.dt));
+  return by_type(a.dt, [&](auto t) {
+    hipLaunchKernelGGL(k_distill_apply<decltype(t)>, grid_of((int64_t)a.T * chunks), dim3(kGradThreads), 0, st, a, sp, chunks, len);
+  });
 }
 
 hipError_t launch_distill_bwd(const TokenArgs& args, hipStream_t st) {
   TokenArgs a = args;
   a.stream = streams(a);
-  // a workgroup reads its row's list once for several tiles, while there are workgroups enough
+  // a workgroup reads its row's list once for several tiles, while there are workgroups enough (511x131071 f32 with its
+  // forward 184 to 192 us for 512 to 4096 workgroups, 212 for 8192)
   const int tile = grad_steps(kTileSteps) * (a.dt == BF16 ? 8 : 4);
   const int64_t tiles = (a.V + tile - 1) / tile;
   const int len = tile * (int)std::min<int64_t>(16, std::max<int64_t>(1, tiles * a.T / 4096));

@@ -369,11 +369,13 @@ def test_many_long_rows(V, dt, pad):
         check_distill(zt, z, t_ids, t_z, tail=tail, w=w, dt=dt)
 
 
+@pytest.mark.parametrize("T", [515, 640])
 @pytest.mark.parametrize("V,dt,pad", [(65541, "f32", 0), (131071, "f32", 1), (140001, "bf16", 1)])
-def test_long_rows_whole(V, dt, pad):
-    """The same for the log-probabilities with more rows still (some of them are held to the formula)."""
-    T, H = 515, 12
-    announce(f"long rows whole V={V} {dt}")
+def test_long_rows_whole(V, dt, pad, T):
+    """The same for the log-probabilities with more rows still (some of them are held to the formula), in numbers that go
+    in segments and whole."""
+    H = 12
+    announce(f"long rows T={T} V={V} {dt}")
     rng = np.random.default_rng(V)
     head, tail = gauss(H, V, 16), gauss(3, V, 17)
     head[0, : V // 2 + 100] = -INF
@@ -450,6 +452,48 @@ def test_rows_in_segments(V, dt, pad):
         lt = lse + 0.2 if tail else None
         check_distill(zt, z, t_ids, t_z, tail=tail, lse=lt, dt=dt)
         check_distill(zt[few], z[few], t_ids[few], t_z[few], tail=tail, lse=lt[few] if tail else None, dt=dt)
+
+
+@pytest.mark.parametrize("V,dt,pad", [(65541, "f32", 3), (140001, "bf16", 1)])
+def test_distill_gradient_of_segments(V, dt, pad):
+    """The distillation's gradient after segments, for numbers of rows that do not fill the CUs (some of the rows are held
+    to the formula): lists over several segments, repeated and absent entries, masks; in place and apart, and the backward
+    alone, which reads the list again."""
+    T, K, H = 260, 30, 14
+    announce(f"distillation gradient of segments V={V} {dt}")
+    rng = np.random.default_rng(V)
+    head = gauss(H, V, 21)
+    head[0, : V // 2 + 100] = -INF
+    head[1] = -INF
+    head[2, V - 1] = 40.0
+    zt = torch.empty((T, V + pad), dtype=tdt(dt), device="cuda")[:, :V]
+    zt.normal_()
+    zt[:H] = torch.as_tensor(head).to(tdt(dt))
+    keep = zt.clone()
+    z = zt[:H].double().cpu().numpy()
+    t_ids = rng.integers(0, V, (T, K))
+    t_ids[3, 1:6] = t_ids[3, 0]
+    t_ids[4] = -1
+    t_ids[5, :4] = [0, V - 1, V // 2, -100]
+    t_z, w = rng.standard_normal((T, K)) - 4.0, rng.standard_normal(T)
+    w[6] = 0.0
+    ids, tz, wd = i32(t_ids), f32(t_z), f32(w)
+    loss, st = torch.empty(T, device="cuda"), torch.empty((T, 4), device="cuda")
+    for mode in (0, 1):
+        got = []
+        for dz in (torch.empty((T, V + 2), dtype=zt.dtype, device="cuda")[:, :V], zt):
+            B().poet_distill(zt, ids, tz, loss, st, mode=mode, dloss=wd, dlogits=dz)
+            got.append(dz.clone())
+        zt.copy_(keep)
+        B().poet_distill_bwd(zt, ids, tz, st, wd, zt, mode=mode)
+        got.append(zt.clone())
+        zt.copy_(keep)
+        ref, err, dref, derr = R.distill(z, 1.0, t_ids[:H], tz.double().cpu().numpy()[:H], 1.0, bool(mode), None,
+                                         wd.double().cpu().numpy()[:H])
+        close(loss[:H], ref, err + 2 * R.U * np.abs(np.where(np.isfinite(ref), ref, 0)), "loss")
+        for g in got:
+            close(g[:H], dref, derr + R.HALF[dt] * np.abs(dref) * 1.01 + 1e-38, "dlogits")
+        assert torch.equal(got[0], got[1])
 
 
 def test_more_rows_than_workgroups():
