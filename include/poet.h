@@ -429,8 +429,8 @@ typedef struct poet_logits {
  *   dlogp, dentropy [T] float32 in, nullable (dlogp needs ids): upstream gradients known before the call. With either
  *   of them dlogits [T x V] (dtype of the logits, pitch ldd) receives
  *     dz_j = s ( dlogp (delta_{j, ids} - p_j) - dentropy p_j (log p_j + H) ),
- *   the same as poet_token_logprobs_bwd writes after the forward, from one reading of the logits where a row fits in a
- *   workgroup's registers. Without them dlogits must be NULL. The alternatives carry no gradient. */
+ *   the same (to the rounding of the row's sums) as poet_token_logprobs_bwd writes after the forward, from one reading of
+ *   the logits where a row fits in a workgroup's registers. Without them dlogits must be NULL. The alternatives carry no gradient. */
 size_t poet_token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t dtype, int32_t K);
 poet_status poet_token_logprobs(const poet_logits* L, const void* logits, const int32_t* ids, int32_t K,
                                 const float* dlogp, const float* dentropy, float* logp, float* entropy,
