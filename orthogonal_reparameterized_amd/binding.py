@@ -785,9 +785,15 @@ def _device_of(t, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a GPU tensor")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
     return dev
+
+
+def _current_device() -> int:
+    """The current device once a GPU tensor exists (torch.cuda.current_device() without its look at the initialization)."""
+    get = getattr(_torch()._C, "_cuda_getDevice", None)
+    return get() if get is not None else _torch().cuda.current_device()
 
 
 def _refuse(t, name: str, dev: int):
@@ -810,6 +816,10 @@ def _mat(t, name: str, rows: int, cols: int, dtype, dev: int):
     """(device pointer, row pitch in elements) of a rows x cols tensor with unit column stride; None: (None, 0)."""
     if t is None:
         return None, 0
+    if type(t) is _torch_module.Tensor and t.get_device() == dev and t.dtype is dtype and t.shape == (rows, cols):
+        ld, unit = t.stride()
+        if unit == 1 and ld >= cols:
+            return t.data_ptr(), ld
     if not isinstance(t, _torch().Tensor) or t.get_device() != dev:
         _refuse(t, name, dev)
     if t.dtype != dtype:
